@@ -66,7 +66,7 @@ def draw(rng):
         K = 1 if dense else rng.randint(1, min(8, E))
         c = _case(
             kind, E=E, K=K, R=1 if dense else 2 ** rng.randint(0, 2),
-            T=_spread(rng, 1, 512 if kind.startswith("tokens") else 16384),
+            T=_spread(rng, 1, 128 if kind.startswith("tokens") else 16384),
             H=_spread(rng, 128, 7168, 128 if fp8 else 8), I=_spread(rng, 128, 4096, 128 if fp8 else 8),
             act=rng.choice(ACTS), bias=rng.random() < 0.5, residual=kind != "backward" and rng.random() < 0.5,
             zipf=rng.choice((0.0, 0.0, 1.2)), empty=0.0 if dense else rng.choice((0.0, 0.0, 0.1)))
