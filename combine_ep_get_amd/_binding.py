@@ -26,13 +26,24 @@ EP_MAX_EXPERTS = 2048
 EP_MAX_EXPERTS_PER_RANK = 256
 EP_MAX_TOPK = 32
 EP_MAX_HIDDEN = 1 << 24
+EP_MAX_FEATURES = 1 << 16
+EP_MOE_TOKENS_MAX = 128
+
+EP_ACT_NONE = 0
+EP_ACT_RELU = 1
+EP_ACT_GELU = 2
+EP_ACT_SILU = 3
+EP_ACT_SWIGLU = 4
+EP_ACT_GEGLU = 5
 
 # Every function the C header declares, checked by the test-suite.
 EXPORTS = ("ep_workspace_bytes", "ep_rank_stride_hint", "ep_get_layout", "ep_dispatch",
            "ep_layout_dispatch", "ep_combine", "ep_quantize_fp8", "ep_dispatch_fp8",
            "ep_layout_dispatch_fp8", "ep_get_group_layout", "ep_dispatch_hier", "ep_combine_hier",
            "ep_combine_topk_weights", "ep_read_status", "ep_error_string",
-           "ep_layout_dispatch_noalloc")
+           "ep_layout_dispatch_noalloc", "ep_combine_backward", "ep_expert_product",
+           "ep_expert_product_fp8", "ep_product_workspace_bytes", "ep_expert_product_backward",
+           "ep_moe_tokens_workspace_bytes", "ep_moe_tokens", "ep_moe_tokens_fp8")
 
 
 class EpError(RuntimeError):
@@ -62,6 +73,25 @@ class Problem(ctypes.Structure):
     @property
     def num_rows(self) -> int:
         return self.num_ranks * self.rank_stride_rows
+
+
+class Product(ctypes.Structure):
+    """``ep_product``: inputs C, outputs N and the activation of the experts' products."""
+    _fields_ = [
+        ("in_features", ctypes.c_int32),
+        ("out_features", ctypes.c_int32),
+        ("activation", ctypes.c_int32),
+        ("reserved", ctypes.c_int32),
+    ]
+
+    @classmethod
+    def make(cls, C, N, activation=EP_ACT_NONE):
+        return cls(C, N, activation, 0)
+
+    @property
+    def weight_rows(self) -> int:
+        """M: rows of an expert's weight, both halves of a gated activation."""
+        return self.out_features * (2 if self.activation in (EP_ACT_SWIGLU, EP_ACT_GEGLU) else 1)
 
 
 _lib = None
@@ -106,6 +136,23 @@ def load():
         lib.ep_combine_hier.argtypes = [P, vp, vp, vp, vp, i64, vp, vp, vp]
         lib.ep_combine_topk_weights.restype = ctypes.c_int
         lib.ep_combine_topk_weights.argtypes = [P] + [vp] * 3 + [vp]
+        Q = ctypes.POINTER(Product)
+        lib.ep_combine_backward.restype = ctypes.c_int
+        lib.ep_combine_backward.argtypes = [P] + [vp] * 6 + [vp]
+        lib.ep_expert_product.restype = ctypes.c_int
+        lib.ep_expert_product.argtypes = [P, Q] + [vp] * 8 + [vp]
+        lib.ep_expert_product_fp8.restype = ctypes.c_int
+        lib.ep_expert_product_fp8.argtypes = [P, Q] + [vp] * 2 + [i64, i64] + [vp] * 7 + [vp]
+        lib.ep_product_workspace_bytes.restype = sz
+        lib.ep_product_workspace_bytes.argtypes = [P, Q]
+        lib.ep_expert_product_backward.restype = ctypes.c_int
+        lib.ep_expert_product_backward.argtypes = [P, Q] + [vp] * 12 + [sz, vp]
+        lib.ep_moe_tokens_workspace_bytes.restype = sz
+        lib.ep_moe_tokens_workspace_bytes.argtypes = [P, Q]
+        lib.ep_moe_tokens.restype = ctypes.c_int
+        lib.ep_moe_tokens.argtypes = [P, Q] + [vp] * 10 + [sz, vp]
+        lib.ep_moe_tokens_fp8.restype = ctypes.c_int
+        lib.ep_moe_tokens_fp8.argtypes = [P, Q] + [vp] * 12 + [sz, vp]
         lib.ep_read_status.restype = ctypes.c_int
         lib.ep_read_status.argtypes = [vp, vp]
         lib.ep_error_string.restype = ctypes.c_char_p
@@ -383,6 +430,112 @@ def ep_combine_topk_weights(problem, recv_weight, token_slot, combined_topk_weig
         _arg(token_slot, "token_slot", "int32", T * K),
         _arg(combined_topk_weights, "combined_topk_weights", "float",
         T * K), _stream(stream)), bind)
+
+
+def ep_combine_backward(problem, dout, y, token_slot, topk_weights, dy=None, dweights=None, stream=None,
+                        bind=False):
+    """Gradient of ep_combine: dy (which may be y) and the top-k weights' gradients."""
+    T, H, K, _, _, _, rows = _sizes(problem)
+    return _run("ep_combine_backward", problem, (_arg(dout, "dout", "bf16", T * H),
+        _arg(y, "y", "bf16", rows * H), _arg(token_slot, "token_slot", "int32", T * K),
+        _arg(topk_weights, "topk_weights", "float", T * K), _arg(dy, "dy", "bf16", rows * H),
+        _arg(dweights, "dweights", "float", T * K), _stream(stream)), bind)
+
+
+def _product_sizes(problem, product, expert_count):
+    """E, C, N, M and the rows of x and out: the receive buffer's, or T for a
+    dense product (no expert arrays)."""
+    rows = problem.num_ranks * problem.rank_stride_rows if expert_count is not None else problem.num_tokens
+    return problem.num_experts, product.in_features, product.out_features, product.weight_rows, rows
+
+
+def _product_ref(product, bind):
+    """The product by reference; a bound call keeps a copy of its own."""
+    return ctypes.byref(Product.from_buffer_copy(product) if bind else product)
+
+
+def ep_expert_product(problem, product, x, expert_count, expert_offset, weight, bias=None, residual=None, pre=None,
+                      out=None, stream=None, bind=False):
+    """out = act(x W[e]^T + bias[e]) + residual on the experts' rows; `pre`
+    takes the pre-activations that the backward call reads."""
+    E, C, N, M, rows = _product_sizes(problem, product, expert_count)
+    return _run("ep_expert_product", problem, (_product_ref(product, bind), _arg(x, "x", "bf16", rows * C),
+        _arg(expert_count, "expert_count", "int32", E), _arg(expert_offset, "expert_offset", "int32", E),
+        _arg(weight, "weight", "bf16", E * M * C), _arg(bias, "bias", "float", E * M),
+        _arg(residual, "residual", "bf16", rows * N), _arg(pre, "pre", "bf16", rows * M),
+        _arg(out, "out", "bf16", rows * N), _stream(stream)), bind)
+
+
+def ep_expert_product_fp8(problem, product, x_fp8, x_sf, sf_token_stride, sf_hidden_stride, expert_count,
+                          expert_offset, w_fp8, w_sf, bias=None, residual=None, out=None, stream=None, bind=False):
+    """ep_expert_product on e4m3 rows and weights with fp32 scales."""
+    E, C, N, M, rows = _product_sizes(problem, product, expert_count)
+    nsf = C // 128
+    span = (rows - 1) * sf_token_stride + (nsf - 1) * sf_hidden_stride + 1 if rows and nsf else 0
+    return _run("ep_expert_product_fp8", problem, (_product_ref(product, bind), _arg(x_fp8, "x_fp8", "e4m3", rows * C),
+        _arg(x_sf, "x_sf", "float", span), sf_token_stride, sf_hidden_stride,
+        _arg(expert_count, "expert_count", "int32", E), _arg(expert_offset, "expert_offset", "int32", E),
+        _arg(w_fp8, "w_fp8", "e4m3", E * M * C), _arg(w_sf, "w_sf", "float", E * (M // 128) * nsf),
+        _arg(bias, "bias", "float", E * M), _arg(residual, "residual", "bf16", rows * N),
+        _arg(out, "out", "bf16", rows * N), _stream(stream)), bind)
+
+
+def ep_product_workspace_bytes(problem: Problem, product: Product) -> int:
+    return load().ep_product_workspace_bytes(ctypes.byref(problem), ctypes.byref(product))
+
+
+def ep_expert_product_backward(problem, product, dout, pre, x, expert_count, expert_offset, weight, dpre=None, dx=None,
+                               dweight=None, dweight_acc=None, dbias=None, workspace=None, workspace_bytes=None,
+                               stream=None, bind=False):
+    """Gradients of ep_expert_product: dpre, dx, dweight (bf16) or dweight_acc
+    (fp32, added to), dbias; those that are None are not computed."""
+    E, C, N, M, rows = _product_sizes(problem, product, expert_count)
+    if workspace_bytes is None:
+        workspace_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    return _run("ep_expert_product_backward", problem, (_product_ref(product, bind),
+        _arg(dout, "dout", "bf16", rows * N), _arg(pre, "pre", "bf16", rows * M), _arg(x, "x", "bf16", rows * C),
+        _arg(expert_count, "expert_count", "int32", E), _arg(expert_offset, "expert_offset", "int32", E),
+        _arg(weight, "weight", "bf16", E * M * C), _arg(dpre, "dpre", "bf16", rows * M),
+        _arg(dx, "dx", "bf16", rows * C), _arg(dweight, "dweight", "bf16", E * M * C),
+        _arg(dweight_acc, "dweight_acc", "float", E * M * C), _arg(dbias, "dbias", "float", E * M),
+        _arg(workspace, "workspace", "bytes", workspace_bytes), workspace_bytes, _stream(stream)), bind)
+
+
+def ep_moe_tokens_workspace_bytes(problem: Problem, product: Product) -> int:
+    return load().ep_moe_tokens_workspace_bytes(ctypes.byref(problem), ctypes.byref(product))
+
+
+def _tokens_ptrs(problem, product, x, topk_idx, topk_weights, w1, w1_sf, b1, w2, w2_sf, b2, residual, out, workspace,
+                 workspace_bytes, fp8, stream, bind):
+    T, H, K, E, _, _, _ = _sizes(problem)
+    I, M = product.out_features, product.weight_rows
+    wtype = "e4m3" if fp8 else "bf16"
+    if workspace_bytes is None:
+        workspace_bytes = workspace.numel() * workspace.element_size()
+    sf = lambda t, what, n: (_arg(t, what, "float", n),) if fp8 else ()  # noqa: E731
+    return (_product_ref(product, bind), _arg(x, "x", "bf16", T * H), _arg(topk_idx, "topk_idx", "int32", T * K),
+            _arg(topk_weights, "topk_weights", "float", T * K),
+            _arg(w1, "w1", wtype, E * M * H), *sf(w1_sf, "w1_sf", E * (M // 128) * (H // 128)),
+            _arg(b1, "b1", "float", E * M),
+            _arg(w2, "w2", wtype, E * H * I), *sf(w2_sf, "w2_sf", E * (H // 128) * (I // 128)),
+            _arg(b2, "b2", "float", E * H),
+            _arg(residual, "residual", "bf16", T * H), _arg(out, "out", "bf16", T * H),
+            _arg(workspace, "workspace", "bytes", workspace_bytes), workspace_bytes, _stream(stream))
+
+
+def ep_moe_tokens(problem, product, x, topk_idx, topk_weights, w1, b1, w2, b2, residual, out, workspace,
+                  workspace_bytes=None, stream=None, bind=False):
+    """The whole expert layer for up to EP_MOE_TOKENS_MAX tokens: up product,
+    activation, down product, weighted sum and residual, in two kernels."""
+    return _run("ep_moe_tokens", problem, _tokens_ptrs(problem, product, x, topk_idx, topk_weights, w1, None, b1, w2,
+        None, b2, residual, out, workspace, workspace_bytes, False, stream, bind), bind)
+
+
+def ep_moe_tokens_fp8(problem, product, x, topk_idx, topk_weights, w1_fp8, w1_sf, b1, w2_fp8, w2_sf, b2, residual, out,
+                      workspace, workspace_bytes=None, stream=None, bind=False):
+    """ep_moe_tokens with e4m3 weights and one scale for each 128 x 128 of them."""
+    return _run("ep_moe_tokens_fp8", problem, _tokens_ptrs(problem, product, x, topk_idx, topk_weights, w1_fp8, w1_sf,
+        b1, w2_fp8, w2_sf, b2, residual, out, workspace, workspace_bytes, True, stream, bind), bind)
 
 
 def ep_read_status(workspace, stream=None) -> int:

@@ -15,11 +15,7 @@
 #include "ep_internal.h"
 #include "hier_internal.h"
 
-namespace {
-
-using epget::WsLayout;
-
-bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+namespace epget {
 
 // Checks every field that does not depend on S.
 int check_shape(const ep_problem *p) {
@@ -42,7 +38,7 @@ int check_shape(const ep_problem *p) {
     // the chunk table is read through raw buffer loads with 32-bit byte
     // offsets, and an offset past the table (0xFFFFFFFC) must stay out of
     // range for predicated loads: fewer than 2^30 table entries
-    const WsLayout w = epget::ws_layout(p->num_tokens, p->num_topk, p->num_experts, p->num_ranks,
+    const WsLayout w = ws_layout(p->num_tokens, p->num_topk, p->num_experts, p->num_ranks,
                                         p->num_groups);
     if (w.nchunks * w.pitch >= (int64_t{1} << 30)) return EP_ERR_INVALID_ARG;
     return EP_OK;
@@ -55,6 +51,16 @@ int check_problem(const ep_problem *p) {
     if (p->rank_stride_rows * p->num_ranks > INT32_MAX) return EP_ERR_INVALID_ARG;
     return EP_OK;
 }
+
+}  // namespace epget
+
+namespace {
+
+using epget::check_problem;
+using epget::check_shape;
+using epget::WsLayout;
+
+bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
 int hip_rc(hipError_t e) { return e == hipSuccess ? EP_OK : EP_ERR_HIP; }
 

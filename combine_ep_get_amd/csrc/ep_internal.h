@@ -5,7 +5,14 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+struct ep_problem;
+
 namespace epget {
+
+// Checks of a problem (EP_OK or EP_ERR_INVALID_ARG): every field that does not
+// depend on the slice stride S, and all of them.
+int check_shape(const ep_problem *p);
+int check_problem(const ep_problem *p);
 
 // Entries (token, top-k pairs) per layout chunk.  One wave walks a chunk in
 // 64-entry steps when it assigns slots, and the count tables hold one row per

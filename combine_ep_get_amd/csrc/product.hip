@@ -1,0 +1,528 @@
+// Grouped matrix products over the experts' rows, for gfx950.
+//
+//   forward      out[r,n] = act(sum_c x[r,c] W[e,n,c] + b[e,n]) + residual[r,n]
+//   grad input   dx[r,c]  = sum_m dpre[r,m] W[e,m,c]
+//   grad weight  dW[e,m,c] = sum_{r of e} dpre[r,m] x[r,c]
+//
+// All three are one tiled product D[feature, token] = sum_k P[feature, k]
+// Q[token, k] on the matrix cores.  "Features" are the contiguous dimension
+// of the result, so that a lane's four results of a 16x16 tile are four
+// neighbours of one row: P is the weight (forward, grad input) or x (grad
+// weight), Q is x or dpre; the tokens of grad weight are the weight's rows m.
+// An operand whose rows are contiguous in k is read from LDS in 16-byte
+// pieces; one whose rows are contiguous in the other dimension is read with
+// the transposing LDS loads, so nothing is transposed in memory.
+//
+// Tiles come from global memory straight to LDS, 16 bytes a lane, in two
+// buffers.  A lane always writes 16 bytes at lane * 16, so the swizzle that
+// keeps LDS reads free of bank conflicts is applied to the address that the
+// lane reads.  Rows past the segment or the operand's end are read as its
+// last one (always in bounds) and never stored; the last step of a k that is
+// no multiple of the step goes through registers, with zeros past the end.
+#include <type_traits>
+
+#include "product_device.h"
+
+namespace epget {
+namespace {
+
+enum Mode { kForward, kGradInput, kGradWeight };
+
+constexpr int kStepBytes = 128;  // of k per row and step: 64 bf16 or 128 e4m3
+constexpr int kStepRows = 64;    // k rows per step of an operand contiguous in the other dimension
+
+typedef __attribute__((address_space(3))) char lds_char;
+
+// The operand tile of B rows (contiguous in k) or B columns (not: kStrided)
+// in LDS, B * 128 bytes either way.
+template <int B, bool kStrided>
+struct Tile {
+    static constexpr int kPitch = kStrided ? B * 2 : kStepBytes;
+    static constexpr int kPairs = B / 16;
+    // Strided: the 32-byte pairs of chunks of a row are permuted by these
+    // bits of its index, so that the 16 rows that one transposing load
+    // touches lie in different banks.
+    static __device__ __forceinline__ int pair_mix(int row) { return ((row & 3) | ((row >> 3) & 3) << 2) & (kPairs - 1); }
+
+    // Row of the tile, and the 16-byte chunk of that row, that LDS byte `at` holds.
+    static __device__ __forceinline__ void source(int at, int *row, int *chunk) {
+        *row = at / kPitch;
+        const int pos = (at % kPitch) / 16;
+        *chunk = kStrided ? (((pos >> 1) ^ pair_mix(*row)) << 1) | (pos & 1) : pos ^ (*row & 7);
+    }
+
+    // Fragment of 16 rows (columns) from 16 * f on, k from 32 * ks on: lane
+    // l holds row l & 15 and k = (l >> 4) * 8 .. + 7.
+    static __device__ __forceinline__ bf16x8 fragment(const char *lds, int f, int ks) {
+        const int i = __lane_id() & 15, g = __lane_id() >> 4;
+        if constexpr (kStrided) {
+            typedef short s16x4 __attribute__((ext_vector_type(4)));
+            typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+            union {
+                s16x4 half[2];
+                bf16x8 all;
+            } u;
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const int row = g * 8 + (i >> 2);  // + 32 ks + 4 j, which pair_mix does not see
+                const int at = (row + 32 * ks + 4 * j) * kPitch + ((f ^ pair_mix(row)) << 5) + (i & 3) * 8;
+                u.half[j] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(lds + at));
+            }
+            return u.all;
+        } else {
+            return *reinterpret_cast<const bf16x8 *>(lds + (16 * f + i) * kPitch + (((ks * 4 + g) ^ (i & 7)) << 4));
+        }
+    }
+};
+
+// What a workgroup knows of one operand of its tile: the uniform base
+// address, each lane's offsets from it, and the bytes from step to step.
+template <int B, bool kStrided, int NW>
+struct Operand {
+    static constexpr int kLoads = B * kStepBytes / (NW * 1024);
+    const char *base;
+    uint32_t off[kLoads];
+    int64_t step;
+
+    static __device__ __forceinline__ int lds_at(int i) { return (i * NW + (threadIdx.x >> 6)) * 1024; }
+
+    __device__ __forceinline__ void load(char *lds, int s) const {
+        const char *b = base + s * step;
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i)
+            __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)(b + off[i]),
+                                             (__attribute__((address_space(3))) void *)(lds + lds_at(i)), 16, 0, 0);
+    }
+
+    // The last step, of `left` k (bytes if contiguous in k, rows if not).
+    __device__ __forceinline__ void load_tail(char *lds, int s, int left) const {
+        const char *b = base + s * step;
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+            const int at = lds_at(i) + static_cast<int>(__lane_id()) * 16;
+            int row, chunk;
+            Tile<B, kStrided>::source(at, &row, &chunk);
+            u32x4 v = {0, 0, 0, 0};
+            if ((kStrided ? row : chunk * 16) < left) v = *reinterpret_cast<const u32x4 *>(b + off[i]);
+            *reinterpret_cast<u32x4 *>(lds + at) = v;
+        }
+    }
+};
+
+__device__ __forceinline__ void wait_loads_and_sync() {
+    __builtin_amdgcn_s_waitcnt(kWaitVmcnt0);  // this wave's loads to LDS have landed
+    __syncthreads();
+}
+
+// P's row of LDS row lr in the forward product: with a gated activation the
+// 16-row fragments alternate between the gate's rows and the other half's,
+// so that one lane holds both values of an output.
+template <bool GATED>
+__device__ __forceinline__ int weight_row(int lr, int n0, int N) {
+    if constexpr (GATED) return ((lr >> 4) & 1) * N + min(n0 + (lr >> 5) * 16 + (lr & 15), N - 1);
+    return min(n0 + lr, N - 1);
+}
+
+template <int MODE, int ACT, bool FP8, int WF, int WT, int FF, int TF, class Args>
+__global__ __launch_bounds__(64 * WF * WT) void product_kernel(Args a) {
+    constexpr int NT = 64 * WF * WT, NW = WF * WT;
+    constexpr int BF = WF * FF * 16, BT = WT * TF * 16;
+    constexpr bool kPs = MODE != kForward, kQs = MODE == kGradWeight;
+    constexpr bool GATED = MODE == kForward && act_gated(ACT);
+    constexpr int BN = GATED ? BF / 2 : BF;  // outputs of a tile
+    constexpr int EL = FP8 ? 1 : 2;
+    __shared__ __attribute__((aligned(1024))) char p0[BF * kStepBytes], q0[BT * kStepBytes];
+    __shared__ __attribute__((aligned(1024))) char p1[BF * kStepBytes], q1[BT * kStepBytes];
+    __shared__ int first[MODE == kGradWeight ? 1 : EP_MAX_EXPERTS + 1];
+    __shared__ int wave_sum[NW];
+
+    const int F = MODE == kForward ? a.N : a.C;  // features
+    const int nf = (F + BN - 1) / BN;
+    const int nt_w = (a.M + BT - 1) / BT;  // grad weight: row tiles of a weight
+    int64_t total;
+    if constexpr (MODE == kGradWeight) {
+        total = static_cast<int64_t>(a.seg.E) * nt_w * nf;
+    } else {
+        tile_prefix<NT>(a.seg, BT, first, wave_sum);
+        total = static_cast<int64_t>(first[a.seg.E]) * nf;
+    }
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wf = wave % WF, wt = wave / WF;
+    const int lane = __lane_id(), li = lane & 15, lg = lane >> 4;
+    const int G = gridDim.x;
+
+    for (int64_t round = 0; round * G < total; ++round) {
+        const int64_t tile = tile_of(total, round, blockIdx.x, G);
+        if (tile < 0) break;
+        int e, tt, ft;
+        if constexpr (MODE == kGradWeight) {
+            const int64_t per = static_cast<int64_t>(nt_w) * nf;
+            e = static_cast<int>(tile / per);
+            tile_in_expert(tile - e * per, nt_w, nf, &tt, &ft);
+        } else {
+            e = tile_expert(first, a.seg.E, static_cast<int>(tile / nf));
+            const int f0 = __builtin_amdgcn_readfirstlane(first[e]);
+            const int nt = __builtin_amdgcn_readfirstlane(first[e + 1]) - f0;
+            tile_in_expert(tile - static_cast<int64_t>(f0) * nf, nt, nf, &tt, &ft);
+        }
+        int64_t row0;
+        const int rows = segment(a.seg, e, &row0);
+        const int n0 = ft * BN;  // first feature
+        const int t0 = tt * BT;  // first token of the segment, or weight row
+
+        Operand<BF, kPs, NW> p;
+        Operand<BT, kQs, NW> q;
+        int64_t k_total;  // in bytes, or in rows for grad weight
+        if constexpr (MODE == kForward) {
+            k_total = static_cast<int64_t>(a.C) * EL;
+            p.base = static_cast<const char *>(a.weight) + static_cast<int64_t>(e) * a.M * a.C * EL;
+            q.base = static_cast<const char *>(a.x) + (row0 + t0) * a.C * EL;
+            p.step = q.step = kStepBytes;
+        } else if constexpr (MODE == kGradInput) {
+            k_total = static_cast<int64_t>(a.M) * 2;
+            p.base = reinterpret_cast<const char *>(a.weight) + static_cast<int64_t>(e) * a.M * a.C * 2;
+            q.base = reinterpret_cast<const char *>(a.dpre) + (row0 + t0) * a.M * 2;
+            p.step = static_cast<int64_t>(kStepRows) * a.C * 2;
+            q.step = kStepBytes;
+        } else {
+            k_total = rows;
+            p.base = reinterpret_cast<const char *>(a.x) + row0 * a.C * 2;
+            q.base = reinterpret_cast<const char *>(a.dpre) + row0 * a.M * 2;
+            p.step = static_cast<int64_t>(kStepRows) * a.C * 2;
+            q.step = static_cast<int64_t>(kStepRows) * a.M * 2;
+        }
+#pragma unroll
+        for (int i = 0; i < p.kLoads; ++i) {
+            int row, chunk;
+            Tile<BF, kPs>::source(p.lds_at(i) + lane * 16, &row, &chunk);
+            if constexpr (kPs)  // rows of k, columns of features
+                p.off[i] = static_cast<uint32_t>(row) * (a.C * 2) + min(n0 * 2 + chunk * 16, a.C * 2 - 16);
+            else
+                p.off[i] = static_cast<uint32_t>(weight_row<GATED>(row, n0, a.N)) * (a.C * EL) + chunk * 16;
+        }
+#pragma unroll
+        for (int i = 0; i < q.kLoads; ++i) {
+            int row, chunk;
+            Tile<BT, kQs>::source(q.lds_at(i) + lane * 16, &row, &chunk);
+            if constexpr (kQs)
+                q.off[i] = static_cast<uint32_t>(row) * (a.M * 2) + min(t0 * 2 + chunk * 16, a.M * 2 - 16);
+            else
+                q.off[i] = static_cast<uint32_t>(min(row, rows - 1 - t0)) * (MODE == kForward ? a.C * EL : a.M * 2) +
+                           chunk * 16;
+        }
+
+        f32x4 acc[FF][TF];
+#pragma unroll
+        for (int f = 0; f < FF; ++f)
+#pragma unroll
+            for (int t = 0; t < TF; ++t) acc[f][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+
+        // FP8: the scales of this wave's tokens (one a lane and fragment) and
+        // features (one for each half: outputs are whole blocks of 128)
+        const float *sf_row[TF], *sf_w[2] = {nullptr, nullptr};
+        if constexpr (FP8) {
+#pragma unroll
+            for (int t = 0; t < TF; ++t)
+                sf_row[t] = a.x_sf + (row0 + min(t0 + (wt * TF + t) * 16 + li, rows - 1)) * a.sf_ts;
+            const int kb = a.C / 128;
+            // the wave's first output; past N in a tile's unused part
+            const int nw = min(n0 + wf * (GATED ? FF * 8 : FF * 16), a.N - 1);
+            sf_w[0] = a.w_sf + (static_cast<int64_t>(e) * (a.M / 128) + nw / 128) * kb;
+            sf_w[1] = GATED ? sf_w[0] + static_cast<int64_t>(a.N / 128) * kb : sf_w[0];
+        }
+        float sx[TF], sw[2];
+        auto scales = [&](int s) {
+            if constexpr (FP8) {
+#pragma unroll
+                for (int t = 0; t < TF; ++t) sx[t] = sf_row[t][s * a.sf_hs];
+                sw[0] = sf_w[0][s];
+                sw[1] = sf_w[1][s];
+            }
+        };
+
+        auto compute = [&](const char *pl, const char *ql) {
+            if constexpr (FP8) {
+                union Frag {
+                    bf16x8 half[2];
+                    i32x8 all;
+                };
+                Frag qf[TF];
+#pragma unroll
+                for (int t = 0; t < TF; ++t)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) qf[t].half[h] = Tile<BT, false>::fragment(ql, wt * TF + t, h);
+#pragma unroll
+                for (int f = 0; f < FF; ++f) {
+                    Frag pf;
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) pf.half[h] = Tile<BF, false>::fragment(pl, wf * FF + f, h);
+#pragma unroll
+                    for (int t = 0; t < TF; ++t) {
+                        const f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
+                        // block scales of one (127 is 2^0): the fp32 scales follow in fp32
+                        const f32x4 d = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                            pf.all, qf[t].all, zero, 0, 0, 0, 0x7F7F7F7F, 0, 0x7F7F7F7F);
+                        const float scale = sx[t] * sw[GATED ? f & 1 : 0];
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) acc[f][t][r] = __builtin_fmaf(d[r], scale, acc[f][t][r]);
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int ks = 0; ks < 2; ++ks) {
+                    bf16x8 qf[TF];
+#pragma unroll
+                    for (int t = 0; t < TF; ++t) qf[t] = Tile<BT, kQs>::fragment(ql, wt * TF + t, ks);
+#pragma unroll
+                    for (int f = 0; f < FF; ++f) {
+                        const bf16x8 pf = Tile<BF, kPs>::fragment(pl, wf * FF + f, ks);
+#pragma unroll
+                        for (int t = 0; t < TF; ++t)
+                            acc[f][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(pf, qf[t], acc[f][t], 0, 0, 0);
+                    }
+                }
+            }
+        };
+
+        constexpr int kUnit = MODE == kGradWeight ? kStepRows : kStepBytes;
+        const int full = static_cast<int>(k_total / kUnit), left = static_cast<int>(k_total - static_cast<int64_t>(full) * kUnit);
+        const int steps = full + (left > 0);
+        auto fetch = [&](char *pl, char *ql, int s) {
+            if (s < full) {
+                p.load(pl, s);
+                q.load(ql, s);
+            } else {
+                // k of grad input is bytes of dpre, rows of the weight
+                p.load_tail(pl, s, MODE == kGradInput ? left / 2 : left);
+                q.load_tail(ql, s, left);
+            }
+        };
+        __syncthreads();  // the previous tile's readers are done
+        if (steps > 0) fetch(p0, q0, 0);
+        for (int s = 0; s < steps; s += 2) {
+            wait_loads_and_sync();
+            scales(s);
+            if (s + 1 < steps) fetch(p1, q1, s + 1);
+            compute(p0, q0);
+            if (s + 1 >= steps) break;
+            wait_loads_and_sync();
+            scales(s + 1);
+            if (s + 2 < steps) fetch(p0, q0, s + 2);
+            compute(p1, q1);
+        }
+
+        // Epilogue: lane holds, of fragment (f, t), token li and features lg * 4 .. + 3.
+#pragma unroll
+        for (int t = 0; t < TF; ++t) {
+            const int tok = t0 + (wt * TF + t) * 16 + li;
+            if (tok >= (MODE == kGradWeight ? a.M : rows)) continue;
+            if constexpr (MODE == kForward) {
+                const int64_t r = row0 + tok;
+#pragma unroll
+                for (int f = 0; f < FF; f += GATED ? 2 : 1) {
+                    const int n = n0 + (GATED ? (wf * FF + f) / 2 : wf * FF + f) * 16 + lg * 4;
+                    if (n >= a.N) continue;
+                    f32x4 v = acc[f][t], u = GATED ? acc[f + (GATED ? 1 : 0)][t] : v;
+                    if (a.bias) {
+                        const float *b = a.bias + static_cast<int64_t>(e) * a.M + n;
+                        v += *reinterpret_cast<const f32x4 *>(b);
+                        if (GATED) u += *reinterpret_cast<const f32x4 *>(b + a.N);
+                    }
+                    if (a.pre) {
+                        uint16_t *o = a.pre + r * a.M + n;
+                        *reinterpret_cast<u32x2 *>(o) = u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+                        if (GATED)
+                            *reinterpret_cast<u32x2 *>(o + a.N) = u32x2{pack_bf16x2(u[0], u[1]), pack_bf16x2(u[2], u[3])};
+                    }
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        v[i] = act_one<ACT>(v[i]);
+                        if (GATED) v[i] *= u[i];
+                    }
+                    if (a.residual) {
+                        const u32x2 res = *reinterpret_cast<const u32x2 *>(a.residual + r * a.N + n);
+                        v += f32x4{bf16_lo(res[0]), bf16_hi(res[0]), bf16_lo(res[1]), bf16_hi(res[1])};
+                    }
+                    *reinterpret_cast<u32x2 *>(a.out + r * a.N + n) =
+                        u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+                }
+            } else {
+                const int64_t at = (MODE == kGradInput ? row0 + tok : static_cast<int64_t>(e) * a.M + tok) * a.C;
+#pragma unroll
+                for (int f = 0; f < FF; ++f) {
+                    const int c = n0 + (wf * FF + f) * 16 + lg * 4;
+                    if (c >= a.C) continue;
+                    const f32x4 v = acc[f][t];
+                    const u32x2 o = {pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+                    if constexpr (MODE == kGradInput) {
+                        *reinterpret_cast<u32x2 *>(a.dx + at + c) = o;
+                    } else if (a.dweight) {
+                        *reinterpret_cast<u32x2 *>(a.dweight + at + c) = o;
+                    }
+                    if constexpr (MODE == kGradWeight) {
+                        if (a.dweight_acc) *reinterpret_cast<f32x4 *>(a.dweight_acc + at + c) += v;
+                    }
+                }
+            }
+        }
+    }
+}
+
+// dpre = dout * act'(pre), and the column sums of dpre in fp32, before it is
+// rounded, for the bias gradient.  One workgroup takes a range of an expert's
+// rows and 256 columns of dout: 32 lanes of 8 columns, 8 rows at a time.
+constexpr int kGradColumns = 256;
+constexpr int kGradRowLanes = 8;
+
+__device__ __forceinline__ void unpack8(const uint16_t *p, float v[8]) {
+    const u32x4 u = *reinterpret_cast<const u32x4 *>(p);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        v[2 * q] = bf16_lo(u[q]);
+        v[2 * q + 1] = bf16_hi(u[q]);
+    }
+}
+
+__device__ __forceinline__ void pack8(uint16_t *p, const float v[8]) {
+    *reinterpret_cast<u32x4 *>(p) =
+        u32x4{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])};
+}
+
+template <int ACT>
+__global__ __launch_bounds__(256) void act_grad_kernel(ProductGradArgs a) {
+    constexpr bool GATED = act_gated(ACT);
+    constexpr int kHalves = GATED ? 2 : 1;
+    __shared__ float sums[kGradRowLanes][kGradColumns];
+    const int e = blockIdx.x / a.splits, split = blockIdx.x % a.splits;
+    int64_t row0;
+    const int rows = segment(a.seg, e, &row0);
+    const int per = (rows + a.splits - 1) / a.splits;
+    const int r0 = static_cast<int>(min(static_cast<int64_t>(split) * per, static_cast<int64_t>(rows)));
+    const int r1 = min(r0 + per, rows);
+    const int lane = threadIdx.x & 31, rl = threadIdx.x >> 5;
+    const int n = blockIdx.y * kGradColumns + lane * 8;
+    float sum[kHalves][8] = {};
+    if (n < a.N) {
+        for (int r = r0 + rl; r < r1; r += kGradRowLanes) {
+            const int64_t row = row0 + r;
+            float d[8], v[8], u[8];
+            unpack8(a.dout + row * a.N + n, d);
+            if constexpr (ACT != EP_ACT_NONE) {
+                unpack8(a.pre + row * a.M + n, v);
+                if (GATED) unpack8(a.pre + row * a.M + a.N + n, u);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float slope = act_slope<ACT>(v[i]);
+                    if (GATED) {
+                        const float du = d[i] * act_one<ACT>(v[i]);
+                        d[i] = d[i] * u[i] * slope;
+                        u[i] = du;
+                    } else {
+                        d[i] *= slope;
+                    }
+                }
+                pack8(a.dpre + row * a.M + n, d);
+                if (GATED) pack8(a.dpre + row * a.M + a.N + n, u);
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                sum[0][i] += d[i];
+                if (GATED) sum[kHalves - 1][i] += u[i];
+            }
+        }
+    }
+    if (!a.dbias) return;
+    const int col = blockIdx.y * kGradColumns + threadIdx.x;
+    float *to = a.splits > 1 ? a.partial + static_cast<int64_t>(blockIdx.x) * a.M : a.dbias + static_cast<int64_t>(e) * a.M;
+#pragma unroll
+    for (int h = 0; h < kHalves; ++h) {
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sums[rl][lane * 8 + i] = sum[h][i];
+        __syncthreads();
+        float total = 0.0f;
+#pragma unroll
+        for (int i = 0; i < kGradRowLanes; ++i) total += sums[i][threadIdx.x];
+        if (col < a.N) to[h * a.N + col] = total;
+    }
+}
+
+// dbias[e,m]: the row ranges' partial sums, in order.
+__global__ __launch_bounds__(256) void bias_join_kernel(const float *__restrict__ partial, float *__restrict__ dbias,
+                                                        int64_t n, int32_t M, int32_t splits) {
+    const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+    if (i >= n) return;
+    const int64_t e = i / M, m = i - e * M;
+    float sum = 0.0f;
+    for (int s = 0; s < splits; ++s) sum += partial[(e * splits + s) * M + m];
+    dbias[i] = sum;
+}
+
+constexpr int kCUs = 256;
+
+template <int MODE, int ACT, bool FP8, int WF, int WT, int FF, int TF, class Args>
+hipError_t launch_tiled(const Args &a, hipStream_t stream) {
+    product_kernel<MODE, ACT, FP8, WF, WT, FF, TF><<<kCUs * 2, 64 * WF * WT, 0, stream>>>(a);
+    return hipGetLastError();
+}
+
+template <bool FP8, class Args>
+hipError_t launch_forward(const Args &a, hipStream_t stream) {
+    switch (a.act) {
+#define EP_ACT_CASE(A) \
+    case A: return launch_tiled<kForward, A, FP8, 2, 2, 4, 4>(a, stream);
+        EP_ACT_CASE(EP_ACT_NONE)
+        EP_ACT_CASE(EP_ACT_RELU)
+        EP_ACT_CASE(EP_ACT_GELU)
+        EP_ACT_CASE(EP_ACT_SILU)
+        EP_ACT_CASE(EP_ACT_SWIGLU)
+        EP_ACT_CASE(EP_ACT_GEGLU)
+#undef EP_ACT_CASE
+        default: return hipErrorInvalidValue;
+    }
+}
+
+}  // namespace
+
+int32_t grad_bias_splits(int64_t mean_rows) {
+    const int64_t s = (mean_rows + 511) / 512;
+    return static_cast<int32_t>(s < 1 ? 1 : s > 64 ? 64 : s);
+}
+
+hipError_t launch_product(const ProductArgs &a, bool fp8, hipStream_t stream) {
+    return fp8 ? launch_forward<true>(a, stream) : launch_forward<false>(a, stream);
+}
+
+hipError_t launch_product_grad(const ProductGradArgs &a, hipStream_t stream) {
+    if (a.act != EP_ACT_NONE || a.dbias) {
+        const dim3 grid(a.seg.E * a.splits, (a.N + kGradColumns - 1) / kGradColumns);
+        switch (a.act) {
+#define EP_ACT_CASE(A) \
+    case A: act_grad_kernel<A><<<grid, 256, 0, stream>>>(a); break;
+            EP_ACT_CASE(EP_ACT_NONE)
+            EP_ACT_CASE(EP_ACT_RELU)
+            EP_ACT_CASE(EP_ACT_GELU)
+            EP_ACT_CASE(EP_ACT_SILU)
+            EP_ACT_CASE(EP_ACT_SWIGLU)
+            EP_ACT_CASE(EP_ACT_GEGLU)
+#undef EP_ACT_CASE
+            default: return hipErrorInvalidValue;
+        }
+        const hipError_t rc = hipGetLastError();
+        if (rc != hipSuccess) return rc;
+    }
+    if (a.dbias && a.splits > 1) {
+        const int64_t n = static_cast<int64_t>(a.seg.E) * a.M;
+        bias_join_kernel<<<static_cast<uint32_t>((n + 255) / 256), 256, 0, stream>>>(a.partial, a.dbias, n, a.M, a.splits);
+        const hipError_t rc = hipGetLastError();
+        if (rc != hipSuccess) return rc;
+    }
+    if (a.dx) {
+        const hipError_t rc = launch_tiled<kGradInput, EP_ACT_NONE, false, 2, 2, 4, 4>(a, stream);
+        if (rc != hipSuccess) return rc;
+    }
+    if (a.dweight || a.dweight_acc) return launch_tiled<kGradWeight, EP_ACT_NONE, false, 2, 2, 4, 4>(a, stream);
+    return hipSuccess;
+}
+
+}  // namespace epget

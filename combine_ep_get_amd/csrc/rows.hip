@@ -17,6 +17,7 @@
 // hardware's packed bf16 conversion).
 #include "../../include/ep_get.h"
 #include "device_common.h"
+#include "product_internal.h"
 
 namespace epget {
 namespace {
@@ -228,6 +229,59 @@ __global__ __launch_bounds__(kNarrowThreads) void combine_narrow_kernel(
         __builtin_nontemporal_store(pack_row(acc), reinterpret_cast<u32x4 *>(out + static_cast<int64_t>(t) * c.H) + col);
 }
 
+// Gradient of the combine: one workgroup takes one token and `per` of its
+// entries.  dy = w * dout is a row copy scaled; the weight's gradient is the
+// dot product of dout with the entry's row of y, summed over the workgroup in
+// a fixed order (lanes by halves, then the waves).  A thread reads its vector of y
+// before it writes the same vector of dy, so dy may be y.
+constexpr int kGradThreads = 256;
+
+__global__ __launch_bounds__(kGradThreads) void combine_backward_kernel(
+    const uint16_t *dout, const uint16_t *y, const int32_t *__restrict__ slot, const float *__restrict__ w,
+    uint16_t *dy, float *__restrict__ dw, int32_t H, int32_t K, int32_t nvec, int32_t per, int64_t num_rows) {
+    __shared__ float part[kGradThreads / 64];
+    const int64_t t = blockIdx.x;
+    const u32x4 *drow = reinterpret_cast<const u32x4 *>(dout + t * H);
+    for (int j = blockIdx.y * per; j < min(K, static_cast<int>(blockIdx.y + 1) * per); ++j) {
+        const int32_t s = slot[t * K + j];
+        const bool ok = slot_ok(s, num_rows);
+        float sum = 0.0f;
+        if (ok) {
+            const float wj = w ? w[t * K + j] : 1.0f;
+            for (int v = threadIdx.x; v < nvec; v += kGradThreads) {
+                const u32x4 d = drow[v];
+                if (dw) {
+                    const u32x4 a = reinterpret_cast<const u32x4 *>(y + s * static_cast<int64_t>(H))[v];
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        sum = __builtin_fmaf(bf16_lo(d[q]), bf16_lo(a[q]), sum);
+                        sum = __builtin_fmaf(bf16_hi(d[q]), bf16_hi(a[q]), sum);
+                    }
+                }
+                if (dy) {
+                    u32x4 o;
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) o[q] = pack_bf16x2(wj * bf16_lo(d[q]), wj * bf16_hi(d[q]));
+                    reinterpret_cast<u32x4 *>(dy + s * static_cast<int64_t>(H))[v] = o;
+                }
+            }
+        }
+        if (dw) {
+#pragma unroll
+            for (int d = 32; d; d >>= 1) sum += __shfl_xor(sum, d);
+            __syncthreads();
+            if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = sum;
+            __syncthreads();
+            if (threadIdx.x == 0) {
+                float total = part[0];
+#pragma unroll
+                for (int i = 1; i < kGradThreads / 64; ++i) total += part[i];
+                dw[t * K + j] = ok ? total : 0.0f;
+            }
+        }
+    }
+}
+
 // combined_topk_weights: one thread per (token, top-k) entry.
 __global__ __launch_bounds__(256) void combine_weights_kernel(CopyParams c, const float *__restrict__ recv_w,
                                                               const int32_t *__restrict__ slot,
@@ -347,6 +401,13 @@ hipError_t launch_combine(const CopyParams &c, const uint16_t *y, const int32_t 
     } else {
         combine_kernel<8><<<grid, threads, 0, stream>>>(y, slot, w, out, c.H, c.K, c.nvec, threads, c.num_rows);
     }
+    return hipGetLastError();
+}
+
+hipError_t launch_combine_backward(const CopyParams &c, const uint16_t *dout, const uint16_t *y, const int32_t *slot,
+                                   const float *w, uint16_t *dy, float *dw, hipStream_t stream) {
+    const dim3 grid(c.T, c.K);
+    combine_backward_kernel<<<grid, kGradThreads, 0, stream>>>(dout, y, slot, w, dy, dw, c.H, c.K, c.nvec, 1, c.num_rows);
     return hipGetLastError();
 }
 

@@ -73,6 +73,20 @@ extern "C" {
 #define EP_MAX_TOPK 32
 #define EP_MAX_HIDDEN (1 << 24)
 
+/* Activations of the experts' products.  The gated ones take two values of
+ * each output, from weight rows n and N + n: act(first) * second. */
+#define EP_ACT_NONE 0
+#define EP_ACT_RELU 1
+#define EP_ACT_GELU 2   /* v * Phi(v), Phi the normal distribution function */
+#define EP_ACT_SILU 3   /* v / (1 + exp(-v)) */
+#define EP_ACT_SWIGLU 4 /* silu(gate) * up */
+#define EP_ACT_GEGLU 5  /* gelu(gate) * up */
+
+/* Largest in_features and out_features of an expert product. */
+#define EP_MAX_FEATURES (1 << 16)
+/* Largest num_tokens of ep_moe_tokens and ep_moe_tokens_fp8. */
+#define EP_MOE_TOKENS_MAX 128
+
 /* Problem description shared by all calls.  Valid when:
  *   T >= 0; H >= 8 and H % 8 == 0 (rows are whole 16-byte vectors);
  *   1 <= E <= 2048; 1 <= R <= 1024; E % R == 0; E / R <= 256;
@@ -95,6 +109,16 @@ typedef struct ep_problem {
     int32_t reserved;         /* must be 0 */
     int64_t rank_stride_rows; /* S: rows per rank slice, the same for every rank */
 } ep_problem;
+
+/* One product of every expert.  C and N are multiples of 8 in
+ * [8, EP_MAX_FEATURES]; the expert's weight has M rows of C values: M = N,
+ * or 2N with a gated activation (the gates' rows first). */
+typedef struct ep_product {
+    int32_t in_features;  /* C */
+    int32_t out_features; /* N */
+    int32_t activation;   /* EP_ACT_* */
+    int32_t reserved;     /* must be 0 */
+} ep_product;
 
 /* Bytes of device workspace ep_get_layout needs for this problem (chunk
  * count tables and the status word), or 0 if the problem is invalid.  The
@@ -355,6 +379,144 @@ int ep_combine_hier(const ep_problem *problem, const uint16_t *y, const int32_t 
 int ep_combine_topk_weights(const ep_problem *problem, const float *recv_weight,
                             const int32_t *token_slot, float *combined_topk_weights,
                             void *stream);
+
+/* Gradient of ep_combine: dy[token_slot[t,j], :] = bf16(w[t,j] * dout[t, :])
+ * and dweights[t,j] = sum_h dout[t,h] * y[token_slot[t,j], h], the sum in fp32
+ * in an order that does not change from call to call.  The gradient of
+ * ep_dispatch is ep_combine with unit weights; with this call and
+ * ep_expert_product_backward the path from combine back to the tokens is
+ * whole.
+ *
+ *   dout         [T,H] bf16 device, 16-byte aligned
+ *   y            [R*S,H] bf16 device, 16-byte aligned; NULL if dweights is
+ *   token_slot   [T,K] int32 device
+ *   topk_weights [T,K] fp32 device, or NULL (unit weights)
+ *   dy           [R*S,H] bf16 device, 16-byte aligned, or NULL; may be y
+ *   dweights     [T,K] fp32 device, or NULL
+ * Slots outside [0, R*S) get dweights 0; rows of dy that no slot names are
+ * left untouched.  Each row is named by one slot at most, as ep_get_layout
+ * leaves them. */
+int ep_combine_backward(const ep_problem *problem, const uint16_t *dout, const uint16_t *y,
+                        const int32_t *token_slot, const float *topk_weights, uint16_t *dy,
+                        float *dweights, void *stream);
+
+/* The experts' products on the receive buffer, between dispatch and combine:
+ * for every row r of expert e
+ *   v[r,m]   = sum_c x[r,c] * weight[e,m,c] + bias[e,m]       (m < M)
+ *   out[r,n] = bf16(act(v)[r,n] + residual[r,n])              (n < N)
+ * with fp32 sums and one rounding.  The rows of expert e are
+ * expert_count[e] rows from row rank(e)*S + expert_offset[e] on, cut off at
+ * the end of its slice, as ep_get_layout leaves them; other rows of x are not
+ * read and of out and pre not written.  problem->hidden and the batch's
+ * size only guide the choice of a kernel.
+ * A dense product is num_experts = num_topk = num_ranks = 1 and NULL for
+ * both arrays: rows [0, T).
+ *
+ *   x             [R*S,C] bf16 device
+ *   expert_count, expert_offset [E] int32 device, or both NULL (above)
+ *   weight        [E,M,C] bf16 device
+ *   bias          [E,M] fp32 device, or NULL
+ *   residual      [R*S,N] bf16 device, or NULL; may be out
+ *   pre           [R*S,M] bf16 device, or NULL: v, rounded, for the backward pass
+ *   out           [R*S,N] bf16 device
+ * All of x, weight, bias, residual, pre and out are 16-byte aligned.  The
+ * result of a row does not depend on the other rows' values. */
+int ep_expert_product(const ep_problem *problem, const ep_product *product, const uint16_t *x,
+                      const int32_t *expert_count, const int32_t *expert_offset,
+                      const uint16_t *weight, const float *bias, const uint16_t *residual,
+                      uint16_t *pre, uint16_t *out, void *stream);
+
+/* ep_expert_product on the rows that ep_dispatch_fp8 leaves: e4m3 codes, the
+ * value of x[r,c] being x_fp8[r,c] * x_sf[r*sf_token_stride +
+ * (c/128)*sf_hidden_stride], and of weight[e,m,c] w_fp8[e,m,c] *
+ * w_sf[e, m/128, c/128].  C and N are multiples of 128.  Products of a block
+ * of 128 are summed by the matrix instruction, the scales applied in fp32.
+ *
+ *   x_fp8 [R*S,C] uint8 device, 16-byte aligned
+ *   x_sf  fp32 device, strides >= 1 as for ep_dispatch_fp8
+ *   w_fp8 [E,M,C] uint8 device, 16-byte aligned
+ *   w_sf  [E,M/128,C/128] fp32 device
+ *   the others as for ep_expert_product */
+int ep_expert_product_fp8(const ep_problem *problem, const ep_product *product,
+                          const uint8_t *x_fp8, const float *x_sf, int64_t sf_token_stride,
+                          int64_t sf_hidden_stride, const int32_t *expert_count,
+                          const int32_t *expert_offset, const uint8_t *w_fp8, const float *w_sf,
+                          const float *bias, const uint16_t *residual, uint16_t *out,
+                          void *stream);
+
+/* Bytes of device workspace that ep_expert_product_backward needs, or 0 if
+ * the problem or product is invalid. */
+size_t ep_product_workspace_bytes(const ep_problem *problem, const ep_product *product);
+
+/* Gradient of ep_expert_product, from dout [R*S,N] bf16 and the `pre` that
+ * the forward call wrote:
+ *   dpre[r,m]      = dout[r,n] * d act / d v_m at pre[r,:]
+ *   dx[r,c]        = bf16(sum_m dpre[r,m] * weight[e,m,c])
+ *   dweight[e,m,c] = sum over the rows r of e of dpre[r,m] * x[r,c]
+ *   dbias[e,m]     = sum over the rows r of e of dpre[r,m]
+ * The gradient of the residual is dout itself.  dpre is rounded to bf16
+ * once, for the matrix products; dbias sums it before that rounding.  Sums
+ * are fp32 in a fixed order.
+ *
+ *   pre         [R*S,M] bf16 device; NULL (and dpre NULL) with EP_ACT_NONE
+ *   x, weight   as in the forward call; x may be NULL without dweight and
+ *               dweight_acc, weight without dx
+ *   dpre        [R*S,M] bf16 device, written; may be pre
+ *   dx          [R*S,C] bf16 device, or NULL
+ *   dweight     [E,M,C] bf16 device, overwritten (0 for an expert without
+ *               rows), or NULL
+ *   dweight_acc [E,M,C] fp32 device, added to, or NULL
+ *   dbias       [E,M] fp32 device, overwritten, or NULL
+ *   workspace   ep_product_workspace_bytes bytes, 256-byte aligned; NULL
+ *               (with 0 bytes) without dbias
+ * bf16 and fp32 arrays are 16-byte aligned. */
+int ep_expert_product_backward(const ep_problem *problem, const ep_product *product,
+                               const uint16_t *dout, const uint16_t *pre, const uint16_t *x,
+                               const int32_t *expert_count, const int32_t *expert_offset,
+                               const uint16_t *weight, uint16_t *dpre, uint16_t *dx,
+                               uint16_t *dweight, float *dweight_acc, float *dbias,
+                               void *workspace, size_t workspace_bytes, void *stream);
+
+/* Bytes of device workspace that ep_moe_tokens and ep_moe_tokens_fp8 need, or
+ * 0 if the problem or product is invalid. */
+size_t ep_moe_tokens_workspace_bytes(const ep_problem *problem, const ep_product *product);
+
+/* The whole expert layer for a few tokens (T <= EP_MOE_TOKENS_MAX), from the
+ * router's output to the combined rows, in two kernels and without a layout,
+ * a receive buffer or a dispatch:
+ *   h[t,j,:]  = act(w1[e] x[t] + b1[e]),  e = topk_idx[t,j]
+ *   out[t,:]  = bf16(residual[t,:] + sum_j topk_weights[t,j] * (w2[e] h[t,j,:] + b2[e]))
+ * Sums are fp32; h is rounded to bf16 once, scaled by its weight.  Results do
+ * not change from call to call.  product->in_features is H, out_features the
+ * experts' inner width I.  problem's R, G, A and S are checked but not used.
+ *
+ *   x            [T,H] bf16 device
+ *   topk_idx     [T,K] int32 device; -1 is an empty entry
+ *   topk_weights [T,K] fp32 device, or NULL (unit weights)
+ *   w1 [E,M,H], w2 [E,H,I] bf16 device (M = I, or 2I when gated)
+ *   b1 [E,M], b2 [E,H] fp32 device, or NULL
+ *   residual     [T,H] bf16 device, or NULL; may be out
+ *   out          [T,H] bf16 device; may be x
+ *   workspace    ep_moe_tokens_workspace_bytes bytes, 256-byte aligned; calls
+ *                that may overlap need one each.  Its first word is the
+ *                status that ep_read_status returns: EP_ERR_BAD_EXPERT if an
+ *                id is outside [0,E) and not -1 (it counts as empty).
+ * An expert that a token names twice counts twice.  x, the weights, b1, b2,
+ * residual and out are 16-byte aligned. */
+int ep_moe_tokens(const ep_problem *problem, const ep_product *product, const uint16_t *x,
+                  const int32_t *topk_idx, const float *topk_weights, const uint16_t *w1,
+                  const float *b1, const uint16_t *w2, const float *b2, const uint16_t *residual,
+                  uint16_t *out, void *workspace, size_t workspace_bytes, void *stream);
+
+/* ep_moe_tokens with e4m3 weights: w1_fp8 [E,M,H] and w2_fp8 [E,H,I] codes
+ * with fp32 scales w1_sf [E,M/128,H/128] and w2_sf [E,H/128,I/128].  H and I
+ * are multiples of 128.  x stays bf16; the codes are widened to bf16, which
+ * holds them exactly. */
+int ep_moe_tokens_fp8(const ep_problem *problem, const ep_product *product, const uint16_t *x,
+                      const int32_t *topk_idx, const float *topk_weights, const uint8_t *w1_fp8,
+                      const float *w1_sf, const float *b1, const uint8_t *w2_fp8,
+                      const float *w2_sf, const float *b2, const uint16_t *residual,
+                      uint16_t *out, void *workspace, size_t workspace_bytes, void *stream);
 
 /* Synchronises `stream`, then returns the status word the last
  * ep_get_layout on that workspace wrote (EP_OK, EP_ERR_BAD_EXPERT or
