@@ -86,26 +86,31 @@ struct Operand {
 
     static __device__ __forceinline__ int lds_at(int i) { return (i * NW + (threadIdx.x >> 6)) * 1024; }
 
-    __device__ __forceinline__ void load(char *lds, int s) const {
-        const char *b = base + s * step;
+    // The next step's tile.  The base is kept in scalar registers and opaque,
+    // so that each load is one instruction of base and 32-bit offset; the
+    // compiler would otherwise carry a 64-bit address a lane and load.
+    __device__ __forceinline__ void load(char *lds) {
+        asm volatile("" : "+s"(base));
 #pragma unroll
         for (int i = 0; i < kLoads; ++i)
-            __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)(b + off[i]),
+            __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)(base + off[i]),
                                              (__attribute__((address_space(3))) void *)(lds + lds_at(i)), 16, 0, 0);
+        base += step;
     }
 
-    // The last step, of `left` k (bytes if contiguous in k, rows if not).
-    __device__ __forceinline__ void load_tail(char *lds, int s, int left) const {
-        const char *b = base + s * step;
+    // A first step of `left` k only (bytes if contiguous in k, rows if not),
+    // with zeros in its other places.
+    __device__ __forceinline__ void load_part(char *lds, int left) {
 #pragma unroll
         for (int i = 0; i < kLoads; ++i) {
             const int at = lds_at(i) + static_cast<int>(__lane_id()) * 16;
             int row, chunk;
             Tile<B, kStrided>::source(at, &row, &chunk);
             u32x4 v = {0, 0, 0, 0};
-            if ((kStrided ? row : chunk * 16) < left) v = *reinterpret_cast<const u32x4 *>(b + off[i]);
+            if ((kStrided ? row : chunk * 16) < left) v = *reinterpret_cast<const u32x4 *>(base + off[i]);
             *reinterpret_cast<u32x4 *>(lds + at) = v;
         }
+        base += kStrided ? step / kStepRows * left : left;
     }
 };
 
@@ -240,75 +245,127 @@ __global__ __launch_bounds__(64 * WF * WT) void product_kernel(Args a) {
             }
         };
 
-        auto compute = [&](const char *pl, const char *ql) {
-            if constexpr (FP8) {
-                union Frag {
-                    bf16x8 half[2];
-                    i32x8 all;
-                };
-                Frag qf[TF];
+        // A step is computed in phases of half of P's fragments, each with 32
+        // k (bf16: four phases) or all 128 k (FP8: two).  Each phase's
+        // fragments are read from LDS while the phase before it multiplies.
+        constexpr int PF = FF / 2, KS = FP8 ? 2 : 1;
+        union Frag {
+            bf16x8 part[KS];
+            i32x8 all;  // FP8
+        };
+        struct PFrags {
+            Frag f[PF];
+        } pa, pb;
+        struct QFrags {
+            Frag t[TF];
+        } qa, qb;
+        auto read_p = [&](PFrags &h, const char *pl, int ks, int half) {
 #pragma unroll
-                for (int t = 0; t < TF; ++t)
+            for (int f = 0; f < PF; ++f)
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) qf[t].half[h] = Tile<BT, false>::fragment(ql, wt * TF + t, h);
+                for (int k = 0; k < KS; ++k)
+                    h.f[f].part[k] = Tile<BF, kPs>::fragment(pl, wf * FF + half * PF + f, FP8 ? k : ks);
+        };
+        auto read_q = [&](QFrags &h, const char *ql, int ks) {
 #pragma unroll
-                for (int f = 0; f < FF; ++f) {
-                    Frag pf;
+            for (int t = 0; t < TF; ++t)
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) pf.half[h] = Tile<BF, false>::fragment(pl, wf * FF + f, h);
+                for (int k = 0; k < KS; ++k) h.t[t].part[k] = Tile<BT, kQs>::fragment(ql, wt * TF + t, FP8 ? k : ks);
+        };
+        auto multiply = [&](const PFrags &pf, const QFrags &qf, int half) {
 #pragma unroll
-                    for (int t = 0; t < TF; ++t) {
+            for (int f = 0; f < PF; ++f) {
+#pragma unroll
+                for (int t = 0; t < TF; ++t) {
+                    f32x4 &to = acc[half * PF + f][t];
+                    if constexpr (FP8) {
                         const f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
                         // block scales of one (127 is 2^0): the fp32 scales follow in fp32
                         const f32x4 d = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                            pf.all, qf[t].all, zero, 0, 0, 0, 0x7F7F7F7F, 0, 0x7F7F7F7F);
+                            pf.f[f].all, qf.t[t].all, zero, 0, 0, 0, 0x7F7F7F7F, 0, 0x7F7F7F7F);
                         const float scale = sx[t] * sw[GATED ? f & 1 : 0];
 #pragma unroll
-                        for (int r = 0; r < 4; ++r) acc[f][t][r] = __builtin_fmaf(d[r], scale, acc[f][t][r]);
-                    }
-                }
-            } else {
-#pragma unroll
-                for (int ks = 0; ks < 2; ++ks) {
-                    bf16x8 qf[TF];
-#pragma unroll
-                    for (int t = 0; t < TF; ++t) qf[t] = Tile<BT, kQs>::fragment(ql, wt * TF + t, ks);
-#pragma unroll
-                    for (int f = 0; f < FF; ++f) {
-                        const bf16x8 pf = Tile<BF, kPs>::fragment(pl, wf * FF + f, ks);
-#pragma unroll
-                        for (int t = 0; t < TF; ++t)
-                            acc[f][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(pf, qf[t], acc[f][t], 0, 0, 0);
+                        for (int r = 0; r < 4; ++r) to[r] = __builtin_fmaf(d[r], scale, to[r]);
+                    } else {
+                        to = __builtin_amdgcn_mfma_f32_16x16x32_bf16(pf.f[f].part[0], qf.t[t].part[0], to, 0, 0, 0);
                     }
                 }
             }
+            __builtin_amdgcn_sched_barrier(0);
         };
 
+        // A part step comes first, if k is no multiple of the step.
         constexpr int kUnit = MODE == kGradWeight ? kStepRows : kStepBytes;
-        const int full = static_cast<int>(k_total / kUnit), left = static_cast<int>(k_total - static_cast<int64_t>(full) * kUnit);
+        const int full = static_cast<int>(k_total / kUnit);
+        const int left = static_cast<int>(k_total - static_cast<int64_t>(full) * kUnit);
         const int steps = full + (left > 0);
-        auto fetch = [&](char *pl, char *ql, int s) {
-            if (s < full) {
-                p.load(pl, s);
-                q.load(ql, s);
-            } else {
-                // k of grad input is bytes of dpre, rows of the weight
-                p.load_tail(pl, s, MODE == kGradInput ? left / 2 : left);
-                q.load_tail(ql, s, left);
-            }
+        auto fetch = [&](char *pl, char *ql) {
+            p.load(pl);
+            q.load(ql);
         };
-        __syncthreads();  // the previous tile's readers are done
-        if (steps > 0) fetch(p0, q0, 0);
-        for (int s = 0; s < steps; s += 2) {
-            wait_loads_and_sync();
+        // One step, with Q's first fragments in q0f: when every wave has read
+        // all of this buffer and the next step's loads have landed, the loads
+        // of the step after that start into this buffer, and the next step's
+        // first fragments are read into q1f (FP8) or q0f during the last phase.
+        auto step = [&](char *pl, char *ql, char *pn, char *qn, QFrags &q0f, QFrags &q1f, int s, auto fetch_more,
+                        auto more) {
             scales(s);
-            if (s + 1 < steps) fetch(p1, q1, s + 1);
-            compute(p0, q0);
-            if (s + 1 >= steps) break;
-            wait_loads_and_sync();
-            scales(s + 1);
-            if (s + 2 < steps) fetch(p0, q0, s + 2);
-            compute(p1, q1);
+            read_p(pb, pl, 0, 1);
+            multiply(pa, q0f, 0);
+            if constexpr (!FP8) {
+                read_q(q1f, ql, 1);
+                read_p(pa, pl, 1, 0);
+                multiply(pb, q0f, 1);
+                read_p(pb, pl, 1, 1);
+                multiply(pa, q1f, 0);
+            }
+            if constexpr (more()) {
+                wait_loads_and_sync();
+                if constexpr (fetch_more()) fetch(pl, ql);
+                read_q(FP8 ? q1f : q0f, qn, 0);
+                read_p(pa, pn, 0, 0);
+            }
+            multiply(pb, FP8 ? q0f : q1f, 1);
+        };
+        constexpr std::true_type yes{};
+        constexpr std::false_type no{};
+        if (steps > 0) {
+            __syncthreads();  // the previous tile's readers are done
+            // steps alternate between the buffers and end in the second one
+            auto first_step = [&](char *pl, char *ql, char *pn, char *qn, QFrags &qf) {
+                if (left > 0) {
+                    // k of grad input is bytes of dpre, rows of the weight
+                    p.load_part(pl, MODE == kGradInput ? left / 2 : left);
+                    q.load_part(ql, left);
+                } else {
+                    fetch(pl, ql);
+                }
+                wait_loads_and_sync();
+                if (steps > 1) fetch(pn, qn);
+                read_q(qf, ql, 0);
+                read_p(pa, pl, 0, 0);
+            };
+            int s = 0;
+            if (steps & 1) {
+                first_step(p1, q1, p0, q0, qb);
+                if (steps == 1) {
+                    step(p1, q1, p0, q0, qb, qa, 0, no, no);
+                } else {
+                    step(p1, q1, p0, q0, qb, qa, 0, yes, yes);
+                    if (!FP8) qa = qb;
+                }
+                s = 1;
+            } else {
+                first_step(p0, q0, p1, q1, qa);
+            }
+            for (; s + 2 < steps; s += 2) {
+                step(p0, q0, p1, q1, qa, qb, s, yes, yes);
+                step(p1, q1, p0, q0, FP8 ? qb : qa, FP8 ? qa : qb, s + 1, yes, yes);
+            }
+            if (s < steps) {
+                step(p0, q0, p1, q1, qa, qb, s, no, yes);
+                step(p1, q1, p0, q0, FP8 ? qb : qa, FP8 ? qa : qb, s + 1, no, no);
+            }
         }
 
         // Epilogue: lane holds, of fragment (f, t), token li and features lg * 4 .. + 3.
@@ -462,15 +519,27 @@ constexpr int kCUs = 256;
 
 template <int MODE, int ACT, bool FP8, int WF, int WT, int FF, int TF, class Args>
 hipError_t launch_tiled(const Args &a, hipStream_t stream) {
-    product_kernel<MODE, ACT, FP8, WF, WT, FF, TF><<<kCUs * 2, 64 * WF * WT, 0, stream>>>(a);
+    // persistent workgroups: as many as the CUs' LDS holds (two buffers of both tiles)
+    constexpr int kPerCU = WF * WT > 4 ? 1 : 2;
+    product_kernel<MODE, ACT, FP8, WF, WT, FF, TF><<<kCUs * kPerCU, 64 * WF * WT, 0, stream>>>(a);
     return hipGetLastError();
+}
+
+template <int MODE, int ACT, bool FP8, class Args>
+hipError_t launch_sized(const Args &a, hipStream_t stream) {
+    if constexpr (FP8) {
+        return launch_tiled<MODE, ACT, true, 4, 2, 4, 4>(a, stream);
+    } else {
+        if (a.mean_rows >= 160) return launch_tiled<MODE, ACT, false, 2, 4, 8, 4>(a, stream);
+        return launch_tiled<MODE, ACT, false, 2, 2, 4, 4>(a, stream);
+    }
 }
 
 template <bool FP8, class Args>
 hipError_t launch_forward(const Args &a, hipStream_t stream) {
     switch (a.act) {
 #define EP_ACT_CASE(A) \
-    case A: return launch_tiled<kForward, A, FP8, 2, 2, 4, 4>(a, stream);
+    case A: return launch_sized<kForward, A, FP8>(a, stream);
         EP_ACT_CASE(EP_ACT_NONE)
         EP_ACT_CASE(EP_ACT_RELU)
         EP_ACT_CASE(EP_ACT_GELU)
@@ -518,10 +587,10 @@ hipError_t launch_product_grad(const ProductGradArgs &a, hipStream_t stream) {
         if (rc != hipSuccess) return rc;
     }
     if (a.dx) {
-        const hipError_t rc = launch_tiled<kGradInput, EP_ACT_NONE, false, 2, 2, 4, 4>(a, stream);
+        const hipError_t rc = launch_sized<kGradInput, EP_ACT_NONE, false>(a, stream);
         if (rc != hipSuccess) return rc;
     }
-    if (a.dweight || a.dweight_acc) return launch_tiled<kGradWeight, EP_ACT_NONE, false, 2, 2, 4, 4>(a, stream);
+    if (a.dweight || a.dweight_acc) return launch_sized<kGradWeight, EP_ACT_NONE, false>(a, stream);
     return hipSuccess;
 }
 
