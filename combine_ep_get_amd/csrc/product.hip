@@ -89,10 +89,11 @@ struct Operand {
     // The next step's tile.  The base is kept in scalar registers and opaque,
     // so that each load is one instruction of base and 32-bit offset; the
     // compiler would otherwise carry a 64-bit address a lane and load.
+    template <int N = kLoads>
     __device__ __forceinline__ void load(char *lds) {
         asm volatile("" : "+s"(base));
 #pragma unroll
-        for (int i = 0; i < kLoads; ++i)
+        for (int i = 0; i < N; ++i)
             __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)(base + off[i]),
                                              (__attribute__((address_space(3))) void *)(lds + lds_at(i)), 16, 0, 0);
         base += step;
@@ -126,6 +127,17 @@ template <bool GATED>
 __device__ __forceinline__ int weight_row(int lr, int n0, int N) {
     if constexpr (GATED) return ((lr >> 4) & 1) * N + min(n0 + (lr >> 5) * 16 + (lr & 15), N - 1);
     return min(n0 + lr, N - 1);
+}
+
+// Calls f with the constant `live`, 1 to N.
+template <int N, class F>
+__device__ __forceinline__ void accumulate_fewer(int live, F &f) {
+    if constexpr (N > 0) {
+        if (live == N)
+            f(std::integral_constant<int, N>{});
+        else
+            accumulate_fewer<N - 1>(live, f);
+    }
 }
 
 template <int MODE, int ACT, bool FP8, int WF, int WT, int FF, int TF, class Args>
@@ -173,7 +185,15 @@ __global__ __launch_bounds__(64 * WF * WT) void product_kernel(Args a) {
         int64_t row0;
         const int rows = segment(a.seg, e, &row0);
         const int n0 = ft * BN;  // first feature
-        const int t0 = tt * BT;  // first token of the segment, or weight row
+        // The tokens are spread evenly over the tiles: each wave computes
+        // `live` of its TF fragments of 16, the same number in all tiles.
+        // Experts of 512 rows on average have 3 tiles of 256 as often as 2,
+        // the third nearly empty.
+        const int tokens = MODE == kGradWeight ? a.M : rows;
+        const int tiles = (tokens + BT - 1) / BT;
+        const int live = ((tokens + tiles - 1) / tiles + WT * 16 - 1) / (WT * 16);
+        const int t0 = tt * live * (WT * 16);  // first token of the segment, or weight row
+        if (t0 >= tokens) continue;            // rounded up, the tiles before hold all of them
 
         Operand<BF, kPs, NW> p;
         Operand<BT, kQs, NW> q;
@@ -228,7 +248,7 @@ __global__ __launch_bounds__(64 * WF * WT) void product_kernel(Args a) {
         if constexpr (FP8) {
 #pragma unroll
             for (int t = 0; t < TF; ++t)
-                sf_row[t] = a.x_sf + (row0 + min(t0 + (wt * TF + t) * 16 + li, rows - 1)) * a.sf_ts;
+                sf_row[t] = a.x_sf + (row0 + min(t0 + (wt * live + t) * 16 + li, rows - 1)) * a.sf_ts;
             const int kb = a.C / 128;
             // the wave's first output; past N in a tile's unused part
             const int nw = min(n0 + wf * (GATED ? FF * 8 : FF * 16), a.N - 1);
@@ -245,6 +265,8 @@ __global__ __launch_bounds__(64 * WF * WT) void product_kernel(Args a) {
             }
         };
 
+        auto accumulate = [&](auto live_fragments) {
+        constexpr int TA = live_fragments();
         // A step is computed in phases of half of P's fragments, each with 32
         // k (bf16: four phases) or all 128 k (FP8: two).  Each phase's
         // fragments are read from LDS while the phase before it multiplies.
@@ -268,15 +290,15 @@ __global__ __launch_bounds__(64 * WF * WT) void product_kernel(Args a) {
         };
         auto read_q = [&](QFrags &h, const char *ql, int ks) {
 #pragma unroll
-            for (int t = 0; t < TF; ++t)
+            for (int t = 0; t < TA; ++t)
 #pragma unroll
-                for (int k = 0; k < KS; ++k) h.t[t].part[k] = Tile<BT, kQs>::fragment(ql, wt * TF + t, FP8 ? k : ks);
+                for (int k = 0; k < KS; ++k) h.t[t].part[k] = Tile<BT, kQs>::fragment(ql, wt * TA + t, FP8 ? k : ks);
         };
         auto multiply = [&](const PFrags &pf, const QFrags &qf, int half) {
 #pragma unroll
             for (int f = 0; f < PF; ++f) {
 #pragma unroll
-                for (int t = 0; t < TF; ++t) {
+                for (int t = 0; t < TA; ++t) {
                     f32x4 &to = acc[half * PF + f][t];
                     if constexpr (FP8) {
                         const f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -301,7 +323,8 @@ __global__ __launch_bounds__(64 * WF * WT) void product_kernel(Args a) {
         const int steps = full + (left > 0);
         auto fetch = [&](char *pl, char *ql) {
             p.load(pl);
-            q.load(ql);
+            // the loads of the live rows: 8 a wave and load
+            q.template load<kQs ? q.kLoads : (WT * TA * 2 + NW - 1) / NW>(ql);
         };
         // One step, with Q's first fragments in q0f: when every wave has read
         // all of this buffer and the next step's loads have landed, the loads
@@ -367,12 +390,18 @@ __global__ __launch_bounds__(64 * WF * WT) void product_kernel(Args a) {
                 step(p1, q1, p0, q0, FP8 ? qb : qa, FP8 ? qa : qb, s + 1, no, no);
             }
         }
+        };
+        if (live == TF) {
+            accumulate(std::integral_constant<int, TF>{});
+        } else {
+            accumulate_fewer<TF - 1>(live, accumulate);
+        }
 
         // Epilogue: lane holds, of fragment (f, t), token li and features lg * 4 .. + 3.
 #pragma unroll
         for (int t = 0; t < TF; ++t) {
-            const int tok = t0 + (wt * TF + t) * 16 + li;
-            if (tok >= (MODE == kGradWeight ? a.M : rows)) continue;
+            const int tok = t0 + (wt * live + t) * 16 + li;
+            if (t >= live || tok >= tokens) continue;
             if constexpr (MODE == kForward) {
                 const int64_t r = row0 + tok;
 #pragma unroll
