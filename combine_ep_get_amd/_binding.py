@@ -161,18 +161,24 @@ def load():
     return _lib
 
 
-# Element types the C calls read, by the C type of the argument.
+# Element types the C calls read, by the C type of the argument (filled on
+# first use, so that importing the package does not import torch).
+_DTYPES: dict = {}
+
+
 def _dtypes():
-    import torch
-    return {
-        "int32": (torch.int32,),
-        "int64": (torch.int64,),
-        "float": (torch.float32,),
-        "uint8": (torch.uint8, torch.bool),
-        "bf16": (torch.bfloat16, torch.int16, torch.uint16),
-        "e4m3": (torch.float8_e4m3fn, torch.uint8, torch.int8),
-        "bytes": None,
-    }
+    if not _DTYPES:
+        import torch
+        _DTYPES.update({
+            "int32": (torch.int32,),
+            "int64": (torch.int64,),
+            "float": (torch.float32,),
+            "uint8": (torch.uint8, torch.bool),
+            "bf16": (torch.bfloat16, torch.int16, torch.uint16),
+            "e4m3": (torch.float8_e4m3fn, torch.uint8, torch.int8),
+            "bytes": None,
+        })
+    return _DTYPES
 
 
 def _arg(t, what: str, ctype: str, count: int):
@@ -186,14 +192,14 @@ def _arg(t, what: str, ctype: str, count: int):
         return t
     if not t.is_contiguous():
         raise ValueError(f"{what}: libepget takes contiguous arrays; call .contiguous() first")
-    allowed = _dtypes()[ctype]
+    allowed = (_DTYPES or _dtypes())[ctype]
     if allowed is not None and t.dtype not in allowed:
         raise ValueError(f"{what}: dtype {t.dtype}, expected one of {allowed}")
     have = t.numel() * t.element_size() if allowed is None else t.numel()
     if have < count:
         raise ValueError(f"{what}: {have} {'bytes' if allowed is None else 'elements'}, "
                          f"the call uses {count}")
-    if t.device.type != "cuda":
+    if not t.is_cuda:
         raise ValueError(f"{what}: a {t.device.type} tensor; the library takes device memory")
     return t.data_ptr()
 
@@ -231,8 +237,10 @@ def _fp8_rows_ptrs(problem, x_fp8, x_sf, recv_x_fp8, recv_sf, sf_token_stride, s
 
 def _stream(stream):
     if stream is None:
+        # the raw handle: torch.cuda.current_stream() builds an object around
+        # it, which takes as long as the launch (2.9 us against 0.4)
         import torch
-        return torch.cuda.current_stream().cuda_stream
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream

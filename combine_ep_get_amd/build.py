@@ -7,7 +7,8 @@ import subprocess
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libepget.so")
-SOURCES = ["api.hip", "layout.hip", "rows.hip", "hier.hip", "api_product.hip", "product.hip", "tokens.hip"]
+SOURCES = ["api.hip", "layout.hip", "rows.hip", "hier.hip", "api_product.hip", "product.hip", "few.hip",
+           "tokens.hip"]
 # bandwidth probes the benchmark compares the kernels with (not the path)
 PROBE_LIB = os.path.join(HERE, "libepprobe.so")
 PROBE_SOURCES = ["probe.hip"]

@@ -1,0 +1,104 @@
+// Expert products of few rows, for gfx950: the weights are the traffic.
+//
+//   out[r,n] = act(sum_c x[r,c] W[e,n,c] + b[e,n]) + residual[r,n]
+//
+// One workgroup takes up to 16 TF rows of an expert and 16 outputs (32 weight
+// rows when gated), its waves the blocks of k in turn; the sums are joined in
+// LDS in a fixed order.  A tile of the tiled product would spend its LDS traffic and
+// barriers on rows that are not there, and its grid of 128 outputs a
+// workgroup leaves most of the chip idle on one small product.
+#include <type_traits>
+
+#include "few_device.h"
+
+namespace epget {
+namespace {
+
+template <int ACT, bool FP8, int TF>
+__global__ __launch_bounds__(kFewThreads) void product_few_kernel(ProductArgs a) {
+    constexpr bool GATED = act_gated(ACT);
+    constexpr int FF = GATED ? 2 : 1;
+    __shared__ int first[EP_MAX_EXPERTS + 1];
+    __shared__ int wave_sum[kFewWaves];
+    __shared__ f32x4 part[kFewWaves][FF][TF][64];
+    tile_prefix<kFewThreads>(a.seg, 16 * TF, first, wave_sum);
+    const int lane = __lane_id(), li = lane & 15, lg = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int nf = (a.N + 15) / 16;
+    const int64_t total = static_cast<int64_t>(first[a.seg.E]) * nf;
+    const int64_t pitch = static_cast<int64_t>(a.C) * (FP8 ? 1 : 2);
+    for (int64_t round = 0; round * gridDim.x < total; ++round) {
+        const int64_t tile = tile_of(total, round, blockIdx.x, gridDim.x);
+        if (tile < 0) break;
+        const int e = tile_expert(first, a.seg.E, static_cast<int>(tile / nf));
+        const int f0 = __builtin_amdgcn_readfirstlane(first[e]);
+        const int nt = __builtin_amdgcn_readfirstlane(first[e + 1]) - f0;
+        int tt, ft;
+        tile_in_expert(tile - static_cast<int64_t>(f0) * nf, nt, nf, &tt, &ft);
+        int64_t row0;
+        const int rows = segment(a.seg, e, &row0);
+        const int n0 = ft * 16, t0 = tt * 16 * TF;
+        const char *row[FF], *col[TF];
+        const float *w_sf[FF], *x_sf[TF];
+#pragma unroll
+        for (int f = 0; f < FF; ++f) {
+            const int64_t r = static_cast<int64_t>(e) * a.M + f * a.N + min(n0 + li, a.N - 1);
+            row[f] = static_cast<const char *>(a.weight) + r * pitch;
+            w_sf[f] = FP8 ? a.w_sf + (static_cast<int64_t>(e) * (a.M / 128) + (f * a.N + n0) / 128) * (a.C / 128) : nullptr;
+        }
+        f32x4 acc[FF][TF];
+#pragma unroll
+        for (int t = 0; t < TF; ++t) {
+            const int64_t r = row0 + min(t0 + t * 16 + li, rows - 1);
+            col[t] = static_cast<const char *>(a.x) + r * pitch;
+            x_sf[t] = FP8 ? a.x_sf + r * a.sf_ts : nullptr;
+#pragma unroll
+            for (int f = 0; f < FF; ++f) acc[f][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        }
+        accumulate_blocks<FP8, FP8>(acc, row, col, w_sf, x_sf, a.sf_hs, a.C, wave, kFewWaves, lg);
+#pragma unroll
+        for (int f = 0; f < FF; ++f)
+#pragma unroll
+            for (int t = 0; t < TF; ++t) part[wave][f][t][lane] = acc[f][t];
+        __syncthreads();
+        // wave t joins and writes fragment t
+        for (int t = wave; t < TF; t += kFewWaves) {
+            const int tok = t0 + t * 16 + li, n = n0 + lg * 4;
+            if (tok >= rows || n >= a.N) continue;
+            f32x4 v[FF];
+#pragma unroll
+            for (int f = 0; f < FF; ++f) v[f] = sum_waves(&part[0][f][t][lane], FF * TF * 64);
+            write_outputs<ACT>(a, e, row0 + tok, n, v[0], v[FF - 1]);
+        }
+        __syncthreads();
+    }
+}
+
+template <int ACT, bool FP8>
+hipError_t launch_few(const ProductArgs &a, hipStream_t stream) {
+    const uint32_t grid = 1024;
+    if (a.mean_rows <= 16)
+        product_few_kernel<ACT, FP8, 1><<<grid, kFewThreads, 0, stream>>>(a);
+    else
+        product_few_kernel<ACT, FP8, 3><<<grid, kFewThreads, 0, stream>>>(a);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_product_few(const ProductArgs &a, bool fp8, hipStream_t stream) {
+    switch (a.act) {
+#define EP_ACT_CASE(A) \
+    case A: return fp8 ? launch_few<A, true>(a, stream) : launch_few<A, false>(a, stream);
+        EP_ACT_CASE(EP_ACT_NONE)
+        EP_ACT_CASE(EP_ACT_RELU)
+        EP_ACT_CASE(EP_ACT_GELU)
+        EP_ACT_CASE(EP_ACT_SILU)
+        EP_ACT_CASE(EP_ACT_SWIGLU)
+        EP_ACT_CASE(EP_ACT_GEGLU)
+#undef EP_ACT_CASE
+        default: return hipErrorInvalidValue;
+    }
+}
+
+}  // namespace epget

@@ -408,29 +408,7 @@ __global__ __launch_bounds__(64 * WF * WT) void product_kernel(Args a) {
                 for (int f = 0; f < FF; f += GATED ? 2 : 1) {
                     const int n = n0 + (GATED ? (wf * FF + f) / 2 : wf * FF + f) * 16 + lg * 4;
                     if (n >= a.N) continue;
-                    f32x4 v = acc[f][t], u = GATED ? acc[f + (GATED ? 1 : 0)][t] : v;
-                    if (a.bias) {
-                        const float *b = a.bias + static_cast<int64_t>(e) * a.M + n;
-                        v += *reinterpret_cast<const f32x4 *>(b);
-                        if (GATED) u += *reinterpret_cast<const f32x4 *>(b + a.N);
-                    }
-                    if (a.pre) {
-                        uint16_t *o = a.pre + r * a.M + n;
-                        *reinterpret_cast<u32x2 *>(o) = u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
-                        if (GATED)
-                            *reinterpret_cast<u32x2 *>(o + a.N) = u32x2{pack_bf16x2(u[0], u[1]), pack_bf16x2(u[2], u[3])};
-                    }
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        v[i] = act_one<ACT>(v[i]);
-                        if (GATED) v[i] *= u[i];
-                    }
-                    if (a.residual) {
-                        const u32x2 res = *reinterpret_cast<const u32x2 *>(a.residual + r * a.N + n);
-                        v += f32x4{bf16_lo(res[0]), bf16_hi(res[0]), bf16_lo(res[1]), bf16_hi(res[1])};
-                    }
-                    *reinterpret_cast<u32x2 *>(a.out + r * a.N + n) =
-                        u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+                    write_outputs<ACT>(a, e, r, n, acc[f][t], acc[f + (GATED ? 1 : 0)][t]);
                 }
             } else {
                 const int64_t at = (MODE == kGradInput ? row0 + tok : static_cast<int64_t>(e) * a.M + tok) * a.C;
@@ -588,6 +566,7 @@ int32_t grad_bias_splits(int64_t mean_rows) {
 }
 
 hipError_t launch_product(const ProductArgs &a, bool fp8, hipStream_t stream) {
+    if (a.mean_rows <= kFewRows) return launch_product_few(a, fp8, stream);
     return fp8 ? launch_forward<true>(a, stream) : launch_forward<false>(a, stream);
 }
 

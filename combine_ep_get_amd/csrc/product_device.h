@@ -47,6 +47,33 @@ __device__ __forceinline__ float act_slope(float v) {
     return 1.0f;
 }
 
+// Epilogue of four neighbouring outputs n .. n + 3 of row r: v (and, gated, u)
+// are their sums.
+template <int ACT>
+__device__ __forceinline__ void write_outputs(const ProductArgs &a, int e, int64_t r, int n, f32x4 v, f32x4 u) {
+    constexpr bool GATED = act_gated(ACT);
+    if (a.bias) {
+        const float *b = a.bias + static_cast<int64_t>(e) * a.M + n;
+        v += *reinterpret_cast<const f32x4 *>(b);
+        if (GATED) u += *reinterpret_cast<const f32x4 *>(b + a.N);
+    }
+    if (a.pre) {
+        uint16_t *o = a.pre + r * a.M + n;
+        *reinterpret_cast<u32x2 *>(o) = u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+        if (GATED) *reinterpret_cast<u32x2 *>(o + a.N) = u32x2{pack_bf16x2(u[0], u[1]), pack_bf16x2(u[2], u[3])};
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        v[i] = act_one<ACT>(v[i]);
+        if (GATED) v[i] *= u[i];
+    }
+    if (a.residual) {
+        const u32x2 res = *reinterpret_cast<const u32x2 *>(a.residual + r * a.N + n);
+        v += f32x4{bf16_lo(res[0]), bf16_hi(res[0]), bf16_lo(res[1]), bf16_hi(res[1])};
+    }
+    *reinterpret_cast<u32x2 *>(a.out + r * a.N + n) = u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+}
+
 // Rows of expert e, from `row0` on; an expert whose rows run past its slice
 // keeps those inside it (the layout gives the others no slot), and arrays
 // that no layout wrote cannot lead outside the buffer.

@@ -62,6 +62,10 @@ constexpr int kMaxTokens = 128;  // EP_MOE_TOKENS_MAX
 // still spread over the chip.
 int32_t grad_bias_splits(int64_t mean_rows);
 
+// Experts of up to this many rows on average take the product for few rows.
+constexpr int64_t kFewRows = 48;
+
+hipError_t launch_product_few(const ProductArgs &a, bool fp8, hipStream_t stream);
 hipError_t launch_product(const ProductArgs &a, bool fp8, hipStream_t stream);
 hipError_t launch_product_grad(const ProductGradArgs &a, hipStream_t stream);
 hipError_t launch_tokens(const TokensArgs &a, bool fp8, hipStream_t stream);

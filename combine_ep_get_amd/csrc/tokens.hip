@@ -9,28 +9,26 @@
 // tokens, and k is split over the waves of a workgroup in blocks of 128, so
 // that no wave waits for another until the sums are joined in LDS, in a fixed
 // order.  Scaling h by its weight lets the down product sum a token's
-// experts in the accumulators themselves: a column is one token, and an
-// expert that the token does not name multiplies zeros.
+// experts with no further factors.
 //
 // Every workgroup first sorts the entries by expert in LDS: at most
 // kMaxTokens * EP_MAX_TOPK ids, which stay in L2.  A token that names an
 // expert twice keeps one entry, with the sum of both weights.
-#include "product_device.h"
+#include <type_traits>
+
+#include "few_device.h"
 
 namespace epget {
 namespace {
 
-constexpr int kTokThreads = 512;
-constexpr int kTokWaves = kTokThreads / 64;
 constexpr int kMaxEntries = kMaxTokens * EP_MAX_TOPK;
-constexpr int kBlockK = 128;  // k per block: one scale of an FP8 weight, four bf16 matrix instructions
 
 struct EntryLists {
     int end[EP_MAX_EXPERTS];             // end of expert e's run in `entry` (its start is end[e - 1])
     uint16_t expert[kMaxEntries < EP_MAX_EXPERTS ? kMaxEntries : EP_MAX_EXPERTS];  // experts with entries, ascending
     int16_t id[kMaxEntries];             // expert of each entry, -1 for none
     uint16_t entry[kMaxEntries];         // t * K + j, by expert
-    int wave_sum[kTokWaves];
+    int wave_sum[kFewWaves];
     int experts;                         // number of experts with entries
     int bad;
 
@@ -40,10 +38,10 @@ struct EntryLists {
 // Called by the whole workgroup; ends with a barrier.
 __device__ __forceinline__ void sort_entries(const TokensArgs &a, EntryLists &l) {
     const int n = a.T * a.K;
-    for (int e = threadIdx.x; e < a.E; e += kTokThreads) l.end[e] = 0;
+    for (int e = threadIdx.x; e < a.E; e += kFewThreads) l.end[e] = 0;
     if (threadIdx.x == 0) l.bad = 0;
     __syncthreads();
-    for (int i = threadIdx.x; i < n; i += kTokThreads) {
+    for (int i = threadIdx.x; i < n; i += kFewThreads) {
         const int e = a.idx[i];
         const bool ok = e >= 0 && e < a.E;
         l.id[i] = ok ? e : -1;
@@ -57,11 +55,11 @@ __device__ __forceinline__ void sort_entries(const TokensArgs &a, EntryLists &l)
         for (int j = i - i % a.K; j < i; ++j) keep = keep && l.id[j] != e;
         return keep;
     };
-    for (int i = threadIdx.x; i < n; i += kTokThreads)
+    for (int i = threadIdx.x; i < n; i += kFewThreads)
         if (first_of_token(i)) atomicAdd(&l.end[l.id[i]], 1);
     __syncthreads();
     // exclusive sums of the counts (low half) and of the experts with any (high half)
-    const int per = (a.E + kTokThreads - 1) / kTokThreads;
+    const int per = (a.E + kFewThreads - 1) / kFewThreads;
     const int e0 = min(static_cast<int>(threadIdx.x) * per, a.E), e1 = min(e0 + per, a.E);
     int sum = 0;
     for (int e = e0; e < e1; ++e) sum += l.end[e] + (l.end[e] ? 1 << 16 : 0);
@@ -69,7 +67,7 @@ __device__ __forceinline__ void sort_entries(const TokensArgs &a, EntryLists &l)
     if ((threadIdx.x & 63) == 63) l.wave_sum[threadIdx.x >> 6] = incl;
     __syncthreads();
     int before = incl - sum;
-    for (int w = 0; w < kTokWaves; ++w)
+    for (int w = 0; w < kFewWaves; ++w)
         if (w < static_cast<int>(threadIdx.x >> 6)) before += l.wave_sum[w];
     for (int e = e0; e < e1; ++e) {
         const int c = l.end[e];
@@ -77,226 +75,191 @@ __device__ __forceinline__ void sort_entries(const TokensArgs &a, EntryLists &l)
         if (c) l.expert[before >> 16] = static_cast<uint16_t>(e);
         before += c + (c ? 1 << 16 : 0);
     }
-    if (threadIdx.x == kTokThreads - 1) l.experts = before >> 16;
+    if (threadIdx.x == kFewThreads - 1) l.experts = before >> 16;
     __syncthreads();
     // the order inside a run is the hardware's: every entry is a column of
     // its own, whose result does not depend on its place
-    for (int i = threadIdx.x; i < n; i += kTokThreads)
+    for (int i = threadIdx.x; i < n; i += kFewThreads)
         if (first_of_token(i)) l.entry[atomicAdd(&l.end[l.id[i]], 1)] = static_cast<uint16_t>(i);
     __syncthreads();
 }
 
-// A block of 128 k of one weight row fragment, as it comes from memory: bf16
-// in four pieces of 8 k a lane (k = 32 q + 8 g), e4m3 in two of 16 (k = 64 q + 16 g).
-template <bool FP8>
-struct WeightBlock {
-    static constexpr int kPieces = FP8 ? 2 : 4;
-    u32x4 v[kPieces];
+// up: items are (expert with entries, 16 outputs).  With enough items for
+// every wave of the chip, a wave takes an item by itself and waits for no
+// other; else a workgroup does, each wave a share of k, joined in LDS.
+// kWaveItems: items from which waves work alone (8 waves on each of 256 CUs).
+constexpr int kWaveItems = 2048;
 
-    // row: this lane's row; k0: first k; K: end of k (zeros past it)
-    __device__ __forceinline__ void load(const char *row, int k0, int K, int lg) {
+// This lane's sums of columns c0 .. c0 + 16 CF - 1 of expert e's entries and
+// outputs n0 .. n0 + 15 (of both halves when gated) over a share of k.
+template <bool FP8, int FF, int CF>
+__device__ __forceinline__ void up_columns(const TokensArgs &a, const EntryLists &l, f32x4 (&acc)[FF][CF], int e, int c0,
+                                           int m, int s0, int n0, int first, int step) {
+    const int li = __lane_id() & 15, lg = __lane_id() >> 4;
+    const int64_t pitch = static_cast<int64_t>(a.H) * (FP8 ? 1 : 2);
+    const char *row[FF], *col[CF];
+    const float *w_sf[FF], *none[CF];
 #pragma unroll
-        for (int q = 0; q < kPieces; ++q) {
-            const int k = k0 + (FP8 ? 64 * q + 16 * lg : 32 * q + 8 * lg);
-            const char *p = row + static_cast<int64_t>(k) * (FP8 ? 1 : 2);
-            v[q] = k < K ? __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(p)) : u32x4{0, 0, 0, 0};
-        }
+    for (int f = 0; f < FF; ++f) {
+        const int64_t r = static_cast<int64_t>(e) * a.M + f * a.I + min(n0 + li, a.I - 1);
+        row[f] = static_cast<const char *>(a.w1) + r * pitch;
+        w_sf[f] = FP8 ? a.w1_sf + (static_cast<int64_t>(e) * (a.M / 128) + (f * a.I + n0) / 128) * (a.H / 128) : nullptr;
     }
-
-    // Operand of matrix instruction s (0..3) of the block.
-    __device__ __forceinline__ bf16x8 operand(int s) const {
-        if constexpr (!FP8) {
-            return __builtin_bit_cast(bf16x8, v[s]);
-        } else {
-            typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-            bf16x8 o;
 #pragma unroll
-            for (int w = 0; w < 2; ++w) {
-                const uint32_t c = v[s >> 1][(s & 1) * 2 + w];
-                const bf16x2 lo = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c, 1.0f, false);
-                const bf16x2 hi = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c, 1.0f, true);
-                o[4 * w] = lo[0], o[4 * w + 1] = lo[1], o[4 * w + 2] = hi[0], o[4 * w + 3] = hi[1];
-            }
-            return o;
-        }
+    for (int c = 0; c < CF; ++c) {
+        const int en = l.entry[s0 + min(c0 + c * 16 + li, m - 1)];
+        col[c] = reinterpret_cast<const char *>(a.x + static_cast<int64_t>(en / a.K) * a.H);
+        none[c] = nullptr;
+#pragma unroll
+        for (int f = 0; f < FF; ++f) acc[f][c] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     }
-};
-
-// The bf16 operand of the same block: column li, the k that the weight's lanes hold.
-template <bool FP8>
-struct ColumnBlock {
-    u32x4 v[4];
-    __device__ __forceinline__ void load(const uint16_t *col, bool live, int k0, int K, int lg) {
-#pragma unroll
-        for (int s = 0; s < 4; ++s) {
-            const int k = k0 + (FP8 ? 64 * (s >> 1) + 16 * lg + 8 * (s & 1) : 32 * s + 8 * lg);
-            v[s] = live && k < K ? *reinterpret_cast<const u32x4 *>(col + k) : u32x4{0, 0, 0, 0};
-        }
-    }
-};
-
-template <bool FP8>
-__device__ __forceinline__ f32x4 block_product(const WeightBlock<FP8> &w, const ColumnBlock<FP8> &x, f32x4 c) {
-#pragma unroll
-    for (int s = 0; s < 4; ++s)
-        c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w.operand(s), __builtin_bit_cast(bf16x8, x.v[s]), c, 0, 0, 0);
-    return c;
+    accumulate_blocks<FP8, false>(acc, row, col, w_sf, none, 0, a.H, first, step, lg);
 }
 
-// Adds the block's product to acc; an FP8 block's is scaled first.
-template <bool FP8>
-__device__ __forceinline__ void add_block(f32x4 &acc, const WeightBlock<FP8> &w, const ColumnBlock<FP8> &x, float scale) {
-    if constexpr (FP8) {
-        const f32x4 d = block_product<FP8>(w, x, f32x4{0.0f, 0.0f, 0.0f, 0.0f});
-#pragma unroll
-        for (int i = 0; i < 4; ++i) acc[i] = __builtin_fmaf(d[i], scale, acc[i]);
-    } else {
-        acc = block_product<FP8>(w, x, acc);
+// h of this lane's column c of the entries and outputs n0 + 4 lg .. + 3.
+template <int ACT>
+__device__ __forceinline__ void up_write(const TokensArgs &a, const EntryLists &l, int e, int c, int m, int s0, int n0,
+                                         f32x4 v, f32x4 u) {
+    const int n = n0 + (__lane_id() >> 4) * 4;
+    if (c >= m || n >= a.I) return;
+    const int en = l.entry[s0 + c], j0 = en - en % a.K;
+    // the weight of the entry, and of the token's others on this expert
+    float wt = 0.0f;
+    for (int j = j0; j < j0 + a.K; ++j)
+        if (l.id[j] == e) wt += a.w ? a.w[j] : 1.0f;
+    if (a.b1) {
+        const float *b = a.b1 + static_cast<int64_t>(e) * a.M + n;
+        v += *reinterpret_cast<const f32x4 *>(b);
+        if (act_gated(ACT)) u += *reinterpret_cast<const f32x4 *>(b + a.I);
     }
+    float o[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o[i] = wt * (act_one<ACT>(v[i]) * (act_gated(ACT) ? u[i] : 1.0f));
+    *reinterpret_cast<u32x2 *>(a.h + static_cast<int64_t>(en) * a.I + n) =
+        u32x2{pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3])};
 }
 
-// up: items are (expert with entries, 16 outputs), one workgroup each in turn.
 template <int ACT, bool FP8>
-__global__ __launch_bounds__(kTokThreads) void tokens_up_kernel(TokensArgs a) {
-    constexpr bool GATED = act_gated(ACT);
-    constexpr int FF = GATED ? 2 : 1;
+__global__ __launch_bounds__(kFewThreads) void tokens_up_kernel(TokensArgs a) {
+    constexpr int FF = act_gated(ACT) ? 2 : 1;
     __shared__ EntryLists l;
-    __shared__ f32x4 part[kTokWaves][FF][64];
+    __shared__ f32x4 part[kFewWaves][FF][64];
     sort_entries(a, l);
     if (blockIdx.x == 0 && threadIdx.x == 0) *a.status = l.bad ? EP_ERR_BAD_EXPERT : EP_OK;
-    const int lane = __lane_id(), li = lane & 15, lg = lane >> 4;
+    const int lane = __lane_id(), li = lane & 15;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int nf = (a.I + 15) / 16, items = l.experts * nf;
-    const int blocks = (a.H + kBlockK - 1) / kBlockK;
-    const int64_t pitch = static_cast<int64_t>(a.H) * (FP8 ? 1 : 2);
-    for (int item = blockIdx.x; item < items; item += gridDim.x) {
+    const bool alone = items >= kWaveItems;
+    const int G = gridDim.x;
+    for (int item = alone ? blockIdx.x + wave * G : blockIdx.x; item < items; item += alone ? G * kFewWaves : G) {
         const int e = __builtin_amdgcn_readfirstlane(l.expert[item / nf]);
         const int n0 = (item % nf) * 16;
         const int s0 = __builtin_amdgcn_readfirstlane(l.start(e)), m = __builtin_amdgcn_readfirstlane(l.end[e]) - s0;
-        const char *row[FF];
-        const float *scale[FF];
-#pragma unroll
-        for (int f = 0; f < FF; ++f) {
-            const int64_t r = static_cast<int64_t>(e) * a.M + f * a.I + min(n0 + li, a.I - 1);
-            row[f] = static_cast<const char *>(a.w1) + r * pitch;
-            scale[f] = FP8 ? a.w1_sf + (static_cast<int64_t>(e) * (a.M / 128) + (f * a.I + n0) / 128) * (a.H / 128) : nullptr;
-        }
-        for (int c0 = 0; c0 < m; c0 += 16) {
-            const int en = l.entry[s0 + min(c0 + li, m - 1)];
-            const uint16_t *col = a.x + static_cast<int64_t>(en / a.K) * a.H;
-            f32x4 acc[FF];
-#pragma unroll
-            for (int f = 0; f < FF; ++f) acc[f] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-            for (int b = wave; b < blocks; b += kTokWaves) {
-                WeightBlock<FP8> w[FF];
-                ColumnBlock<FP8> x;
-#pragma unroll
-                for (int f = 0; f < FF; ++f) w[f].load(row[f], b * kBlockK, a.H, lg);
-                x.load(col, true, b * kBlockK, a.H, lg);
-#pragma unroll
-                for (int f = 0; f < FF; ++f) add_block<FP8>(acc[f], w[f], x, FP8 ? scale[f][b] : 1.0f);
+        for (int c0 = 0; c0 < m;) {
+            if (alone && m - c0 > 16) {
+                f32x4 acc[FF][2];
+                up_columns<FP8, FF, 2>(a, l, acc, e, c0, m, s0, n0, 0, 1);
+                up_write<ACT>(a, l, e, c0 + li, m, s0, n0, acc[0][0], acc[FF - 1][0]);
+                up_write<ACT>(a, l, e, c0 + 16 + li, m, s0, n0, acc[0][1], acc[FF - 1][1]);
+                c0 += 32;
+                continue;
             }
+            f32x4 acc[FF][1];
+            up_columns<FP8, FF, 1>(a, l, acc, e, c0, m, s0, n0, alone ? 0 : wave, alone ? 1 : kFewWaves);
+            if (!alone) {
 #pragma unroll
-            for (int f = 0; f < FF; ++f) part[wave][f][lane] = acc[f];
-            __syncthreads();
-            if (wave == 0) {
-                f32x4 v[FF];
+                for (int f = 0; f < FF; ++f) part[wave][f][lane] = acc[f][0];
+                __syncthreads();
+                if (wave == 0)
 #pragma unroll
-                for (int f = 0; f < FF; ++f) {
-                    v[f] = part[0][f][lane];
-#pragma unroll
-                    for (int w = 1; w < kTokWaves; ++w) v[f] += part[w][f][lane];
-                }
-                const int n = n0 + lg * 4;
-                if (c0 + li < m && n < a.I) {
-                    // the weight of the entry, and of the token's others on this expert
-                    float wt = 0.0f;
-                    for (int j = en - en % a.K; j < en - en % a.K + a.K; ++j)
-                        if (l.id[j] == e) wt += a.w ? a.w[j] : 1.0f;
-#pragma unroll
-                    for (int f = 0; f < FF; ++f)
-                        if (a.b1) v[f] += *reinterpret_cast<const f32x4 *>(a.b1 + static_cast<int64_t>(e) * a.M + f * a.I + n);
-                    float o[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) o[i] = wt * (act_one<ACT>(v[0][i]) * (GATED ? v[FF - 1][i] : 1.0f));
-                    *reinterpret_cast<u32x2 *>(a.h + static_cast<int64_t>(en) * a.I + n) =
-                        u32x2{pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3])};
-                }
+                    for (int f = 0; f < FF; ++f) acc[f][0] = sum_waves(&part[0][f][lane], FF * 64);
+                __syncthreads();
             }
-            __syncthreads();
+            if (alone || wave == 0) up_write<ACT>(a, l, e, c0 + li, m, s0, n0, acc[0][0], acc[FF - 1][0]);
+            c0 += 16;
         }
     }
 }
 
-// down: one workgroup for each 16 outputs, all experts; TF fragments of 16 tokens.
-template <bool FP8, int TF>
-__global__ __launch_bounds__(kTokThreads) void tokens_down_kernel(TokensArgs a) {
-    __shared__ EntryLists l;
-    __shared__ f32x4 part[kTokWaves][64];
-    sort_entries(a, l);
+// down: one workgroup for each 16 FF outputs, all experts.  Each wave takes
+// whole experts in turn (shares of their k where there are fewer experts than waves): the
+// columns are the expert's entries, and their sums are added to the
+// wave's own sums of every token in LDS, which are joined at the end.  No
+// wave waits for another before that.  sums: [wave][token][16 FF] floats.
+template <bool FP8, int FF, int CF>
+__device__ __forceinline__ void down_columns(const TokensArgs &a, const EntryLists &l, float *sums, int e, int c0, int m,
+                                             int s0, int n0, int first, int step) {
     const int lane = __lane_id(), li = lane & 15, lg = lane >> 4;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int n0 = blockIdx.x * 16;
-    const int blocks = (a.I + kBlockK - 1) / kBlockK, units = l.experts * blocks;
     const int64_t pitch = static_cast<int64_t>(a.I) * (FP8 ? 1 : 2);
-    f32x4 acc[TF];
+    const char *row[FF], *col[CF];
+    const float *w_sf[FF], *none[CF];
+    int tok[CF];
+    f32x4 acc[FF][CF];
 #pragma unroll
-    for (int t = 0; t < TF; ++t) acc[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    for (int u = wave; u < units; u += kTokWaves) {
-        const int o = u / blocks, b = u - o * blocks;
-        const int e = __builtin_amdgcn_readfirstlane(l.expert[o]);
-        const int s0 = __builtin_amdgcn_readfirstlane(l.start(e)), s1 = __builtin_amdgcn_readfirstlane(l.end[e]);
-        WeightBlock<FP8> w;
-        w.load(static_cast<const char *>(a.w2) + (static_cast<int64_t>(e) * a.H + min(n0 + li, a.H - 1)) * pitch,
-               b * kBlockK, a.I, lg);
-        const float scale =
-            FP8 ? a.w2_sf[(static_cast<int64_t>(e) * (a.H / 128) + n0 / 128) * (a.I / 128) + b] : 1.0f;
-        int en[TF];
-#pragma unroll
-        for (int t = 0; t < TF; ++t) en[t] = -1;
-        for (int s = s0; s < s1; ++s) {
-            const int i = l.entry[s], tok = i / a.K;
-#pragma unroll
-            for (int t = 0; t < TF; ++t) en[t] = tok == t * 16 + li ? i : en[t];
-        }
-#pragma unroll
-        for (int t = 0; t < TF; ++t) {
-            if (__ballot(en[t] >= 0) == 0) continue;
-            ColumnBlock<FP8> x;
-            x.load(a.h + static_cast<int64_t>(max(en[t], 0)) * a.I, en[t] >= 0, b * kBlockK, a.I, lg);
-            f32x4 sum = acc[t];
-            add_block<FP8>(sum, w, x, scale);
-            // a token that does not name the expert keeps its sum: zero times
-            // a weight that is not finite is not zero
-#pragma unroll
-            for (int i = 0; i < 4; ++i) acc[t][i] = en[t] >= 0 ? sum[i] : acc[t][i];
-        }
+    for (int f = 0; f < FF; ++f) {
+        const int n = min(n0 + f * 16 + li, a.H - 1);
+        row[f] = static_cast<const char *>(a.w2) + (static_cast<int64_t>(e) * a.H + n) * pitch;
+        w_sf[f] = FP8 ? a.w2_sf + (static_cast<int64_t>(e) * (a.H / 128) + min(n0 + f * 16, a.H - 1) / 128) * (a.I / 128) : nullptr;
     }
 #pragma unroll
-    for (int t = 0; t < TF; ++t) {
-        part[wave][lane] = acc[t];
-        __syncthreads();
-        const int tok = t * 16 + li, n = n0 + lg * 4;
-        if (wave == 0 && tok < a.T && n < a.H) {
-            f32x4 v = part[0][lane];
+    for (int c = 0; c < CF; ++c) {
+        const int en = l.entry[s0 + min(c0 + c * 16 + li, m - 1)];
+        tok[c] = c0 + c * 16 + li < m ? en / a.K : -1;
+        col[c] = reinterpret_cast<const char *>(a.h + static_cast<int64_t>(en) * a.I);
+        none[c] = nullptr;
 #pragma unroll
-            for (int w = 1; w < kTokWaves; ++w) v += part[w][lane];
-            if (a.b2) {
-                for (int j = 0; j < a.K; ++j) {
-                    const int i = tok * a.K + j, e = l.id[i];
-                    if (e < 0) continue;
-                    const float wt = a.w ? a.w[i] : 1.0f;
-                    v += wt * *reinterpret_cast<const f32x4 *>(a.b2 + static_cast<int64_t>(e) * a.H + n);
-                }
-            }
-            const int64_t at = static_cast<int64_t>(tok) * a.H + n;
-            if (a.residual) {
-                const u32x2 r = *reinterpret_cast<const u32x2 *>(a.residual + at);
-                v += f32x4{bf16_lo(r[0]), bf16_hi(r[0]), bf16_lo(r[1]), bf16_hi(r[1])};
-            }
-            *reinterpret_cast<u32x2 *>(a.out + at) = u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+        for (int f = 0; f < FF; ++f) acc[f][c] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    }
+    accumulate_blocks<FP8, false>(acc, row, col, w_sf, none, 0, a.I, first, step, lg);
+#pragma unroll
+    for (int c = 0; c < CF; ++c) {
+        if (tok[c] < 0) continue;
+#pragma unroll
+        for (int f = 0; f < FF; ++f) *reinterpret_cast<f32x4 *>(sums + tok[c] * (16 * FF) + f * 16 + lg * 4) += acc[f][c];
+    }
+}
+
+template <bool FP8, int FF>
+__global__ __launch_bounds__(kFewThreads) void tokens_down_kernel(TokensArgs a) {
+    __shared__ EntryLists l;
+    extern __shared__ __attribute__((aligned(16))) float sums[];
+    sort_entries(a, l);
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int n0 = blockIdx.x * 16 * FF;
+    const int size = a.T * 16 * FF;  // floats of a wave's sums
+    float *mine = sums + wave * size;
+    for (int i = __lane_id() * 4; i < size; i += 256) *reinterpret_cast<f32x4 *>(mine + i) = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    const int shares = l.experts >= kFewWaves ? 1 : l.experts ? kFewWaves / l.experts : 1;
+    for (int u = wave; u < l.experts * shares; u += kFewWaves) {
+        const int e = __builtin_amdgcn_readfirstlane(l.expert[u / shares]);
+        const int s0 = __builtin_amdgcn_readfirstlane(l.start(e)), m = __builtin_amdgcn_readfirstlane(l.end[e]) - s0;
+        for (int c0 = 0; c0 < m; c0 += 32) {
+            if (m - c0 <= 16)
+                down_columns<FP8, FF, 1>(a, l, mine, e, c0, m, s0, n0, u % shares, shares);
+            else
+                down_columns<FP8, FF, 2>(a, l, mine, e, c0, m, s0, n0, u % shares, shares);
         }
-        __syncthreads();
+    }
+    __syncthreads();
+    // four outputs of one token a thread
+    for (int i = threadIdx.x; i < size / 4; i += kFewThreads) {
+        const int tok = i / (4 * FF), n = n0 + (i - tok * (4 * FF)) * 4;
+        if (n >= a.H) continue;
+        f32x4 v = sum_waves(reinterpret_cast<const f32x4 *>(sums) + i, size / 4);
+        if (a.b2) {
+            for (int j = 0; j < a.K; ++j) {
+                const int en = tok * a.K + j, e = l.id[en];
+                if (e < 0) continue;
+                const float wt = a.w ? a.w[en] : 1.0f;
+                v += wt * *reinterpret_cast<const f32x4 *>(a.b2 + static_cast<int64_t>(e) * a.H + n);
+            }
+        }
+        const int64_t at = static_cast<int64_t>(tok) * a.H + n;
+        if (a.residual) {
+            const u32x2 r = *reinterpret_cast<const u32x2 *>(a.residual + at);
+            v += f32x4{bf16_lo(r[0]), bf16_hi(r[0]), bf16_lo(r[1]), bf16_hi(r[1])};
+        }
+        *reinterpret_cast<u32x2 *>(a.out + at) = u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
     }
 }
 
@@ -307,7 +270,7 @@ hipError_t launch_up(const TokensArgs &a, hipStream_t stream) {
     const uint32_t grid = static_cast<uint32_t>(items < 1 ? 1 : items < 1024 ? items : 1024);
     switch (a.act) {
 #define EP_ACT_CASE(A) \
-    case A: tokens_up_kernel<A, FP8><<<grid, kTokThreads, 0, stream>>>(a); break;
+    case A: tokens_up_kernel<A, FP8><<<grid, kFewThreads, 0, stream>>>(a); break;
         EP_ACT_CASE(EP_ACT_NONE)
         EP_ACT_CASE(EP_ACT_RELU)
         EP_ACT_CASE(EP_ACT_GELU)
@@ -322,15 +285,14 @@ hipError_t launch_up(const TokensArgs &a, hipStream_t stream) {
 
 template <bool FP8>
 hipError_t launch_down(const TokensArgs &a, hipStream_t stream) {
-    const uint32_t grid = (a.H + 15) / 16;
-    if (a.T <= 16)
-        tokens_down_kernel<FP8, 1><<<grid, kTokThreads, 0, stream>>>(a);
-    else if (a.T <= 32)
-        tokens_down_kernel<FP8, 2><<<grid, kTokThreads, 0, stream>>>(a);
-    else if (a.T <= 64)
-        tokens_down_kernel<FP8, 4><<<grid, kTokThreads, 0, stream>>>(a);
+    // 32 outputs a workgroup where the tokens' sums fill most of a CU's LDS
+    // anyway, else 16, of which two or more run on a CU
+    const int ff = a.T > 64 ? 2 : 1;
+    const uint32_t grid = (a.H + 16 * ff - 1) / (16 * ff), lds = kFewWaves * a.T * 16 * ff * 4;
+    if (ff == 2)
+        tokens_down_kernel<FP8, 2><<<grid, kFewThreads, lds, stream>>>(a);
     else
-        tokens_down_kernel<FP8, 8><<<grid, kTokThreads, 0, stream>>>(a);
+        tokens_down_kernel<FP8, 1><<<grid, kFewThreads, lds, stream>>>(a);
     return hipGetLastError();
 }
 
