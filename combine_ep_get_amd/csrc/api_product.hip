@@ -136,6 +136,7 @@ int run_product(const ep_problem *p, const ep_product *q, const void *x, const f
     a.residual = residual;
     a.pre = pre;
     a.out = out;
+    a.entries = static_cast<int64_t>(p->num_tokens) * p->num_topk;
     a.mean_rows = mean_rows(p);
     return hip_rc(epget::launch_product(a, fp8, static_cast<hipStream_t>(stream)));
 }

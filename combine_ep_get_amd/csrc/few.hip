@@ -21,7 +21,13 @@ __global__ __launch_bounds__(kFewThreads) void product_few_kernel(ProductArgs a)
     __shared__ int first[EP_MAX_EXPERTS + 1];
     __shared__ int wave_sum[kFewWaves];
     __shared__ f32x4 part[kFewWaves][FF][TF][64];
-    tile_prefix<kFewThreads>(a.seg, 16 * TF, first, wave_sum);
+    if (a.seg.E > 1) {
+        tile_prefix<kFewThreads>(a.seg, 16 * TF, first, wave_sum);
+    } else if (threadIdx.x < 2) {  // no sums over experts: a decode-sized product is mostly latency
+        int64_t row0;
+        first[threadIdx.x] = threadIdx.x ? (segment(a.seg, 0, &row0) + 16 * TF - 1) / (16 * TF) : 0;
+    }
+    __syncthreads();
     const int lane = __lane_id(), li = lane & 15, lg = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int nf = (a.N + 15) / 16;
@@ -55,7 +61,9 @@ __global__ __launch_bounds__(kFewThreads) void product_few_kernel(ProductArgs a)
 #pragma unroll
             for (int f = 0; f < FF; ++f) acc[f][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
         }
-        accumulate_blocks<FP8, FP8>(acc, row, col, w_sf, x_sf, a.sf_hs, a.C, wave, kFewWaves, lg);
+        // neighbouring tiles start at different blocks of k, so that they do
+        // not all read the same piece of x at once (1.5 us of 14)
+        accumulate_blocks<FP8, FP8>(acc, row, col, w_sf, x_sf, a.sf_hs, a.C, (wave + ft) % kFewWaves, kFewWaves, lg);
 #pragma unroll
         for (int f = 0; f < FF; ++f)
 #pragma unroll
@@ -65,23 +73,27 @@ __global__ __launch_bounds__(kFewThreads) void product_few_kernel(ProductArgs a)
         for (int t = wave; t < TF; t += kFewWaves) {
             const int tok = t0 + t * 16 + li, n = n0 + lg * 4;
             if (tok >= rows || n >= a.N) continue;
-            f32x4 v[FF];
-#pragma unroll
-            for (int f = 0; f < FF; ++f) v[f] = sum_waves(&part[0][f][t][lane], FF * TF * 64);
-            write_outputs<ACT>(a, e, row0 + tok, n, v[0], v[FF - 1]);
+            f32x4 v[1] = {sum_waves(&part[0][0][t][lane], FF * TF * 64)};
+            f32x4 u[1] = {GATED ? sum_waves(&part[0][FF - 1][t][lane], FF * TF * 64) : v[0]};
+            write_outputs<ACT>(a, e, row0 + tok, n, v, u);
         }
         __syncthreads();
     }
 }
 
+template <int ACT, bool FP8, int TF>
+hipError_t launch_few(const ProductArgs &a, hipStream_t stream) {
+    // no more workgroups than tiles there can be, each expert's last tile in part filled
+    const int64_t tiles = (a.entries / (16 * TF) + min(static_cast<int64_t>(a.seg.E), a.entries)) * ((a.N + 15) / 16);
+    const uint32_t grid = static_cast<uint32_t>(min(int64_t{1024}, (tiles + 7) / 8 * 8));
+    product_few_kernel<ACT, FP8, TF><<<grid, kFewThreads, 0, stream>>>(a);
+    return hipGetLastError();
+}
+
 template <int ACT, bool FP8>
 hipError_t launch_few(const ProductArgs &a, hipStream_t stream) {
-    const uint32_t grid = 1024;
-    if (a.mean_rows <= 16)
-        product_few_kernel<ACT, FP8, 1><<<grid, kFewThreads, 0, stream>>>(a);
-    else
-        product_few_kernel<ACT, FP8, 3><<<grid, kFewThreads, 0, stream>>>(a);
-    return hipGetLastError();
+    if (a.entries <= 16 * a.seg.E) return launch_few<ACT, FP8, 1>(a, stream);
+    return launch_few<ACT, FP8, 3>(a, stream);
 }
 
 }  // namespace

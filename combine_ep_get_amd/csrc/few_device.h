@@ -146,10 +146,10 @@ __device__ __forceinline__ void accumulate_blocks(f32x4 (&acc)[FF][TF], const ch
                 add_block<WFP8, XFP8>(acc[f][t], o.w[f], o.x[t], XFP8 ? o.sw[f] * o.sx[t] : WFP8 ? o.sw[f] : 1.0f);
     };
     const int full = K / kBlockK;
-    if constexpr (FF * TF < 4) {
+    if constexpr (FF + TF <= 3) {
         pipelined<Block>(first, step, full, [&](Block &o, int b) { load(std::true_type{}, o, b); }, add);
     } else {
-        // two blocks would not fit the registers of a wave
+        // two blocks would take the registers of the second workgroup on a CU
         for (int b = first; b < full; b += step) {
             Block o;
             load(std::true_type{}, o, b);

@@ -120,13 +120,17 @@ __device__ __forceinline__ void wait_loads_and_sync() {
     __syncthreads();
 }
 
-// P's row of LDS row lr in the forward product: with a gated activation the
-// 16-row fragments alternate between the gate's rows and the other half's,
-// so that one lane holds both values of an output.
+// The weight row that LDS row lr (fragment lr / 16) holds in the forward
+// product.  With a gated activation the fragments alternate between the
+// gate's rows and the other half's, so that one lane holds both values of an
+// output.  Two fragments of outputs share 32 neighbours so that a lane's four
+// of each, 8 lg + 4 j + 0..3, are eight in a row: they are stored as 16
+// bytes, and the four lanes of a token as 64.
 template <bool GATED>
 __device__ __forceinline__ int weight_row(int lr, int n0, int N) {
-    if constexpr (GATED) return ((lr >> 4) & 1) * N + min(n0 + (lr >> 5) * 16 + (lr & 15), N - 1);
-    return min(n0 + lr, N - 1);
+    const int f = lr >> (GATED ? 5 : 4), r = lr & 15;
+    const int n = min(n0 + (f >> 1) * 32 + (r >> 2) * 8 + (f & 1) * 4 + (r & 3), N - 1);
+    return GATED && (lr >> 4 & 1) ? N + n : n;
 }
 
 // Calls f with the constant `live`, 1 to N.
@@ -405,10 +409,12 @@ __global__ __launch_bounds__(64 * WF * WT) void product_kernel(Args a) {
             if constexpr (MODE == kForward) {
                 const int64_t r = row0 + tok;
 #pragma unroll
-                for (int f = 0; f < FF; f += GATED ? 2 : 1) {
-                    const int n = n0 + (GATED ? (wf * FF + f) / 2 : wf * FF + f) * 16 + lg * 4;
+                for (int f = 0; f < FF; f += GATED ? 4 : 2) {
+                    const int n = n0 + (GATED ? (wf * FF + f) / 2 : wf * FF + f) * 16 + lg * 8;
                     if (n >= a.N) continue;
-                    write_outputs<ACT>(a, e, r, n, acc[f][t], acc[f + (GATED ? 1 : 0)][t]);
+                    f32x4 v[2] = {acc[f][t], acc[f + (GATED ? 2 : 1)][t]};
+                    f32x4 u[2] = {acc[f + 1][t], acc[f + (GATED ? 3 : 1)][t]};
+                    write_outputs<ACT>(a, e, r, n, v, u);
                 }
             } else {
                 const int64_t at = (MODE == kGradInput ? row0 + tok : static_cast<int64_t>(e) * a.M + tok) * a.C;
@@ -565,8 +571,17 @@ int32_t grad_bias_splits(int64_t mean_rows) {
     return static_cast<int32_t>(s < 1 ? 1 : s > 64 ? 64 : s);
 }
 
+// Which products take the kernel for few rows: experts of up to 8 rows on
+// average, and up to 48 where the tiled product's 128 outputs a workgroup
+// would leave most CUs idle.
+bool few_rows(const ProductArgs &a) {
+    if (a.mean_rows <= 8) return true;
+    const int64_t tiles = a.seg.E * ((a.M + 127) / 128);
+    return a.mean_rows <= 48 && tiles < kCUs;
+}
+
 hipError_t launch_product(const ProductArgs &a, bool fp8, hipStream_t stream) {
-    if (a.mean_rows <= kFewRows) return launch_product_few(a, fp8, stream);
+    if (few_rows(a)) return launch_product_few(a, fp8, stream);
     return fp8 ? launch_forward<true>(a, stream) : launch_forward<false>(a, stream);
 }
 

@@ -47,31 +47,51 @@ __device__ __forceinline__ float act_slope(float v) {
     return 1.0f;
 }
 
-// Epilogue of four neighbouring outputs n .. n + 3 of row r: v (and, gated, u)
-// are their sums.
-template <int ACT>
-__device__ __forceinline__ void write_outputs(const ProductArgs &a, int e, int64_t r, int n, f32x4 v, f32x4 u) {
+// bf16 of 4 G neighbouring values, and back.
+template <int G>
+__device__ __forceinline__ void store_bf16(uint16_t *p, const f32x4 (&v)[G]) {
+    if constexpr (G == 2)
+        *reinterpret_cast<u32x4 *>(p) = u32x4{pack_bf16x2(v[0][0], v[0][1]), pack_bf16x2(v[0][2], v[0][3]),
+                                              pack_bf16x2(v[1][0], v[1][1]), pack_bf16x2(v[1][2], v[1][3])};
+    else
+        *reinterpret_cast<u32x2 *>(p) = u32x2{pack_bf16x2(v[0][0], v[0][1]), pack_bf16x2(v[0][2], v[0][3])};
+}
+
+template <int G>
+__device__ __forceinline__ void add_bf16(f32x4 (&v)[G], const uint16_t *p) {
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+        const u32x2 r = reinterpret_cast<const u32x2 *>(p)[g];
+        v[g] += f32x4{bf16_lo(r[0]), bf16_hi(r[0]), bf16_lo(r[1]), bf16_hi(r[1])};
+    }
+}
+
+// Epilogue of the 4 G neighbouring outputs from n on of row r: v (and, gated,
+// u) are their sums.
+template <int ACT, int G>
+__device__ __forceinline__ void write_outputs(const ProductArgs &a, int e, int64_t r, int n, f32x4 (&v)[G], f32x4 (&u)[G]) {
     constexpr bool GATED = act_gated(ACT);
     if (a.bias) {
-        const float *b = a.bias + static_cast<int64_t>(e) * a.M + n;
-        v += *reinterpret_cast<const f32x4 *>(b);
-        if (GATED) u += *reinterpret_cast<const f32x4 *>(b + a.N);
+        const f32x4 *b = reinterpret_cast<const f32x4 *>(a.bias + static_cast<int64_t>(e) * a.M + n);
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+            v[g] += b[g];
+            if (GATED) u[g] += b[a.N / 4 + g];
+        }
     }
     if (a.pre) {
-        uint16_t *o = a.pre + r * a.M + n;
-        *reinterpret_cast<u32x2 *>(o) = u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
-        if (GATED) *reinterpret_cast<u32x2 *>(o + a.N) = u32x2{pack_bf16x2(u[0], u[1]), pack_bf16x2(u[2], u[3])};
+        store_bf16(a.pre + r * a.M + n, v);
+        if (GATED) store_bf16(a.pre + r * a.M + a.N + n, u);
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        v[i] = act_one<ACT>(v[i]);
-        if (GATED) v[i] *= u[i];
-    }
-    if (a.residual) {
-        const u32x2 res = *reinterpret_cast<const u32x2 *>(a.residual + r * a.N + n);
-        v += f32x4{bf16_lo(res[0]), bf16_hi(res[0]), bf16_lo(res[1]), bf16_hi(res[1])};
-    }
-    *reinterpret_cast<u32x2 *>(a.out + r * a.N + n) = u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+    for (int g = 0; g < G; ++g)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v[g][i] = act_one<ACT>(v[g][i]);
+            if (GATED) v[g][i] *= u[g][i];
+        }
+    if (a.residual) add_bf16(v, a.residual + r * a.N + n);
+    store_bf16(a.out + r * a.N + n, v);
 }
 
 // Rows of expert e, from `row0` on; an expert whose rows run past its slice

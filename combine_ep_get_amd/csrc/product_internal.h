@@ -28,6 +28,7 @@ struct ProductArgs {
     const uint16_t *residual;  // or null
     uint16_t *pre;             // or null
     uint16_t *out;
+    int64_t entries;           // T * K, the most rows there can be
     int64_t mean_rows;         // rows of an average expert, for the choice of the tile
 };
 
@@ -61,9 +62,6 @@ constexpr int kMaxTokens = 128;  // EP_MOE_TOKENS_MAX
 // Row ranges of the bias gradient: enough that a few experts with many rows
 // still spread over the chip.
 int32_t grad_bias_splits(int64_t mean_rows);
-
-// Experts of up to this many rows on average take the product for few rows.
-constexpr int64_t kFewRows = 48;
 
 hipError_t launch_product_few(const ProductArgs &a, bool fp8, hipStream_t stream);
 hipError_t launch_product(const ProductArgs &a, bool fp8, hipStream_t stream);
