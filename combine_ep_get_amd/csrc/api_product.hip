@@ -54,7 +54,7 @@ int64_t mean_rows(const ep_problem *p) {
 }
 
 int64_t grad_workspace(const ep_problem *p, const ep_product *q) {
-    const int64_t splits = epget::grad_bias_splits(mean_rows(p));
+    const int64_t splits = epget::grad_row_ranges(p->num_experts, q->out_features);
     const int64_t floats = splits > 1 ? p->num_experts * splits * weight_rows(q) : 0;
     return 256 + floats * 4;
 }
@@ -219,7 +219,7 @@ int ep_expert_product_backward(const ep_problem *p, const ep_product *q, const u
     a.dbias = dbias;
     a.partial = dbias ? reinterpret_cast<float *>(static_cast<char *>(workspace) + 256) : nullptr;
     a.mean_rows = mean_rows(p);
-    a.splits = epget::grad_bias_splits(a.mean_rows);
+    a.splits = epget::grad_row_ranges(p->num_experts, q->out_features);
     return hip_rc(epget::launch_product_grad(a, static_cast<hipStream_t>(stream)));
 }
 

@@ -59,9 +59,9 @@ struct TokensArgs {
 
 constexpr int kMaxTokens = 128;  // EP_MOE_TOKENS_MAX
 
-// Row ranges of the bias gradient: enough that a few experts with many rows
-// still spread over the chip.
-int32_t grad_bias_splits(int64_t mean_rows);
+// Row ranges that each expert's rows are cut into for the elementwise pass of
+// the backward call; the bias gradients are summed by range, then joined.
+int32_t grad_row_ranges(int32_t E, int32_t N);
 
 hipError_t launch_product_few(const ProductArgs &a, bool fp8, hipStream_t stream);
 hipError_t launch_product(const ProductArgs &a, bool fp8, hipStream_t stream);
