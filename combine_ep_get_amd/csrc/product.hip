@@ -297,13 +297,15 @@ __global__ __launch_bounds__(64 * WF * WT) void product_kernel(Args a) {
             sf_w[0] = a.w_sf + (static_cast<int64_t>(e) * (a.M / 128) + nw / 128) * kb;
             sf_w[1] = GATED ? sf_w[0] + static_cast<int64_t>(a.N / 128) * kb : sf_w[0];
         }
-        float sx[TF], sw[2];
-        auto scales = [&](int s) {
+        struct Scales {
+            float x[TF], w[2];
+        } sa, sb;
+        auto read_scales = [&](Scales &to, int s) {
             if constexpr (FP8) {
 #pragma unroll
-                for (int t = 0; t < TF; ++t) sx[t] = s < 0 ? 0.0f : sf_row[t][s * a.sf_hs];
-                sw[0] = s < 0 ? 0.0f : sf_w[0][s];
-                sw[1] = s < 0 ? 0.0f : sf_w[1][s];
+                for (int t = 0; t < TF; ++t) to.x[t] = sf_row[t][s * a.sf_hs];
+                to.w[0] = sf_w[0][s];
+                to.w[1] = sf_w[1][s];
             }
         };
 
@@ -338,26 +340,39 @@ __global__ __launch_bounds__(64 * WF * WT) void product_kernel(Args a) {
 #pragma unroll
                 for (int k = 0; k < KS; ++k) h.t[t].part[k] = Tile<BT, kQs, false>::fragment(ql, lane, wt * TA + t, FP8 ? k : ks);
         };
-        auto multiply = [&](const PFrags &pf, const QFrags &qf, int half) {
+        auto multiply = [&](const PFrags &pf, const QFrags &qf, const Scales &sc, int half) {
+            if constexpr (FP8) {
+                // A block's products are scaled in fp32 while the matrix unit
+                // does the next fragment's: left to itself, the compiler waits for
+                // each product and scales it at once.
+                f32x4 d[2][TA];
 #pragma unroll
-            for (int f = 0; f < PF; ++f) {
+                for (int f = 0; f <= PF; ++f) {
 #pragma unroll
-                for (int t = 0; t < TA; ++t) {
-                    f32x4 &to = acc[half * PF + f][t];
-                    if constexpr (FP8) {
+                    for (int t = 0; t < TA; ++t) {
                         const f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
-                        // block scales of one (127 is 2^0): the fp32 scales follow in fp32
-                        const f32x4 d = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                            pf.f[f].all, qf.t[t].all, zero, 0, 0, 0, 0x7F7F7F7F, 0, 0x7F7F7F7F);
-                        const float scale = sx[t] * sw[GATED ? f & 1 : 0];
+                        if (f < PF)  // block scales of one (127 is 2^0)
+                            d[f & 1][t] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                                pf.f[f].all, qf.t[t].all, zero, 0, 0, 0, 0x7F7F7F7F, 0, 0x7F7F7F7F);
+                        if (f > 0) {
+                            const float scale = sc.x[t] * sc.w[GATED ? (f - 1) & 1 : 0];
+                            f32x4 &to = acc[half * PF + f - 1][t];
 #pragma unroll
-                        for (int r = 0; r < 4; ++r) to[r] = __builtin_fmaf(d[r], scale, to[r]);
-                    } else {
-                        to = __builtin_amdgcn_mfma_f32_16x16x32_bf16(pf.f[f].part[0], qf.t[t].part[0], to, 0, 0, 0);
+                            for (int r = 0; r < 4; ++r) to[r] = __builtin_fmaf(d[(f - 1) & 1][t][r], scale, to[r]);
+                            __builtin_amdgcn_sched_barrier(0);
+                        }
                     }
+                    __builtin_amdgcn_sched_barrier(0);
                 }
+            } else {
+#pragma unroll
+                for (int f = 0; f < PF; ++f)
+#pragma unroll
+                    for (int t = 0; t < TA; ++t)
+                        acc[half * PF + f][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                            pf.f[f].part[0], qf.t[t].part[0], acc[half * PF + f][t], 0, 0, 0);
+                __builtin_amdgcn_sched_barrier(0);  // phases stay apart: 16 % slower without
             }
-            __builtin_amdgcn_sched_barrier(0);  // phases stay apart: 16 % slower without
         };
 
         // A part step comes first, if k is no multiple of the step.
@@ -377,17 +392,17 @@ __global__ __launch_bounds__(64 * WF * WT) void product_kernel(Args a) {
         // all of this buffer and the next step's loads have landed, the loads
         // of the step after that start into this buffer, and the next step's
         // first fragments are read into q1f (FP8) or q0f during the last phase.
-        auto step = [&](char *pl, char *ql, char *pn, char *qn, QFrags &q0f, QFrags &q1f, int s, auto fetch_more,
-                        auto more) {
-            scales(s - pad);
+        auto step = [&](char *pl, char *ql, char *pn, char *qn, QFrags &q0f, QFrags &q1f, const Scales &sc, Scales &next,
+                        int s, auto fetch_more, auto more) {
+            if constexpr (more()) read_scales(next, s + 1 - pad);  // waited for with the loads to LDS
             read_p(pb, pl, 0, 1);
-            multiply(pa, q0f, 0);
+            multiply(pa, q0f, sc, 0);
             if constexpr (!FP8) {
                 read_q(q1f, ql, 1);
                 read_p(pa, pl, 1, 0);
-                multiply(pb, q0f, 1);
+                multiply(pb, q0f, sc, 1);
                 read_p(pb, pl, 1, 1);
-                multiply(pa, q1f, 0);
+                multiply(pa, q1f, sc, 0);
             }
             if constexpr (more()) {
                 wait_loads_and_sync();
@@ -395,7 +410,7 @@ __global__ __launch_bounds__(64 * WF * WT) void product_kernel(Args a) {
                 read_q(FP8 ? q1f : q0f, qn, 0);
                 read_p(pa, pn, 0, 0);
             }
-            multiply(pb, FP8 ? q0f : q1f, 1);
+            multiply(pb, FP8 ? q0f : q1f, sc, 1);
         };
         constexpr std::true_type yes{};
         constexpr std::false_type no{};
@@ -411,12 +426,18 @@ __global__ __launch_bounds__(64 * WF * WT) void product_kernel(Args a) {
                 }
             };
             if (pad) {
+                if constexpr (FP8) {
+#pragma unroll
+                    for (int t = 0; t < TF; ++t) sa.x[t] = 0.0f;
+                    sa.w[0] = sa.w[1] = 0.0f;
+                }
                 p.load_part(p0, 0);
                 q.load_part(q0, 0);
                 first_step(p1, q1);
                 __syncthreads();
             } else {
                 first_step(p0, q0);
+                read_scales(sa, 0);
                 wait_loads_and_sync();
                 fetch(p1, q1);
             }
@@ -424,11 +445,11 @@ __global__ __launch_bounds__(64 * WF * WT) void product_kernel(Args a) {
             read_p(pa, p0, 0, 0);
             int s = 0;
             for (; s + 2 < total_steps; s += 2) {
-                step(p0, q0, p1, q1, qa, qb, s, yes, yes);
-                step(p1, q1, p0, q0, FP8 ? qb : qa, FP8 ? qa : qb, s + 1, yes, yes);
+                step(p0, q0, p1, q1, qa, qb, sa, sb, s, yes, yes);
+                step(p1, q1, p0, q0, FP8 ? qb : qa, FP8 ? qa : qb, sb, sa, s + 1, yes, yes);
             }
-            step(p0, q0, p1, q1, qa, qb, s, no, yes);
-            step(p1, q1, p0, q0, FP8 ? qb : qa, FP8 ? qa : qb, s + 1, no, no);
+            step(p0, q0, p1, q1, qa, qb, sa, sb, s, no, yes);
+            step(p1, q1, p0, q0, FP8 ? qb : qa, FP8 ? qa : qb, sb, sa, s + 1, no, no);
         }
         };
         if (live == TF) {
@@ -586,7 +607,7 @@ hipError_t launch_sized(const Args &a, hipStream_t stream) {
     if constexpr (FP8) {
         return launch_tiled<MODE, ACT, true, 4, 2, 4, 4>(a, stream);
     } else {
-        if (a.mean_rows >= 160) return launch_tiled<MODE, ACT, false, 2, 4, 8, 4>(a, stream);
+        if (a.mean_rows >= (MODE == kForward ? 160 : 64)) return launch_tiled<MODE, ACT, false, 2, 4, 8, 4>(a, stream);
         return launch_tiled<MODE, ACT, false, 2, 2, 4, 4>(a, stream);
     }
 }
