@@ -229,54 +229,79 @@ __global__ __launch_bounds__(kNarrowThreads) void combine_narrow_kernel(
         __builtin_nontemporal_store(pack_row(acc), reinterpret_cast<u32x4 *>(out + static_cast<int64_t>(t) * c.H) + col);
 }
 
-// Gradient of the combine: one workgroup takes one token and `per` of its
-// entries.  dy = w * dout is a row copy scaled; the weight's gradient is the
-// dot product of dout with the entry's row of y, summed over the workgroup in
-// a fixed order (lanes by halves, then the waves).  A thread reads its vector of y
-// before it writes the same vector of dy, so dy may be y.
-constexpr int kGradThreads = 256;
+// Gradient of the combine: dy = w * dout is a row copy, scaled; a weight's
+// gradient is the dot product of dout with the entry's row of y.  One workgroup
+// takes one token and KG of its entries at a time, with the KG loads of y in
+// flight and dout read once for all of them; the sums are joined over the
+// lanes by halves, then over the waves in order.  y and dy pass once and carry
+// the non-temporal hint.  A thread reads its vector of y before it writes the same
+// vector of dy, so dy may be y.
+//
+// Bound by HBM: 4.0 GB for 16384 tokens of 8 entries and 7168 channels.  With
+// one entry a workgroup dout is read again for each (1113 us against 880),
+// but a batch of under kGradTokens tokens needs the workgroups (128 tokens: 6.8 us).
+constexpr int kGradMaxThreads = 512;
+constexpr int kGradTokens = 1024;
 
-__global__ __launch_bounds__(kGradThreads) void combine_backward_kernel(
+template <int KG>
+__global__ __launch_bounds__(kGradMaxThreads) void combine_backward_kernel(
     const uint16_t *dout, const uint16_t *y, const int32_t *__restrict__ slot, const float *__restrict__ w,
-    uint16_t *dy, float *__restrict__ dw, int32_t H, int32_t K, int32_t nvec, int32_t per, int64_t num_rows) {
-    __shared__ float part[kGradThreads / 64];
+    uint16_t *dy, float *__restrict__ dw, int32_t H, int32_t K, int32_t nvec, int64_t num_rows) {
+    __shared__ float part[kGradMaxThreads / 64][KG];
     const int64_t t = blockIdx.x;
     const u32x4 *drow = reinterpret_cast<const u32x4 *>(dout + t * H);
-    for (int j = blockIdx.y * per; j < min(K, static_cast<int>(blockIdx.y + 1) * per); ++j) {
-        const int32_t s = slot[t * K + j];
-        const bool ok = slot_ok(s, num_rows);
-        float sum = 0.0f;
-        if (ok) {
-            const float wj = w ? w[t * K + j] : 1.0f;
-            for (int v = threadIdx.x; v < nvec; v += kGradThreads) {
-                const u32x4 d = drow[v];
+    const int step = gridDim.y * KG;
+    for (int j0 = blockIdx.y * KG; j0 < K; j0 += step) {
+        int64_t row[KG];
+        bool ok[KG];
+        float wj[KG], sum[KG];
+#pragma unroll
+        for (int j = 0; j < KG; ++j) {
+            const int64_t i = t * K + min(j0 + j, K - 1);
+            const int32_t s = slot[i];
+            ok[j] = j0 + j < K && slot_ok(s, num_rows);
+            row[j] = ok[j] ? s : 0;  // row 0 is in bounds; what comes of it is dropped
+            wj[j] = w ? w[i] : 1.0f;
+            sum[j] = 0.0f;
+        }
+        for (int v = threadIdx.x; v < nvec; v += blockDim.x) {
+            const u32x4 d = drow[v];
+            u32x4 in[KG];
+            if (dw) {
+#pragma unroll
+                for (int j = 0; j < KG; ++j)
+                    in[j] = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(y + row[j] * H) + v);
+            }
+#pragma unroll
+            for (int j = 0; j < KG; ++j) {
                 if (dw) {
-                    const u32x4 a = reinterpret_cast<const u32x4 *>(y + s * static_cast<int64_t>(H))[v];
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
-                        sum = __builtin_fmaf(bf16_lo(d[q]), bf16_lo(a[q]), sum);
-                        sum = __builtin_fmaf(bf16_hi(d[q]), bf16_hi(a[q]), sum);
+                        sum[j] = __builtin_fmaf(bf16_lo(d[q]), bf16_lo(in[j][q]), sum[j]);
+                        sum[j] = __builtin_fmaf(bf16_hi(d[q]), bf16_hi(in[j][q]), sum[j]);
                     }
                 }
-                if (dy) {
+                if (dy && ok[j]) {
                     u32x4 o;
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) o[q] = pack_bf16x2(wj * bf16_lo(d[q]), wj * bf16_hi(d[q]));
-                    reinterpret_cast<u32x4 *>(dy + s * static_cast<int64_t>(H))[v] = o;
+                    for (int q = 0; q < 4; ++q) o[q] = pack_bf16x2(wj[j] * bf16_lo(d[q]), wj[j] * bf16_hi(d[q]));
+                    __builtin_nontemporal_store(o, reinterpret_cast<u32x4 *>(dy + row[j] * H) + v);
                 }
             }
         }
         if (dw) {
+            __syncthreads();  // the round before has been read
 #pragma unroll
-            for (int d = 32; d; d >>= 1) sum += __shfl_xor(sum, d);
+            for (int j = 0; j < KG; ++j) {
+                for (int d = 32; d; d >>= 1) sum[j] += __shfl_xor(sum[j], d);
+                if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6][j] = sum[j];
+            }
             __syncthreads();
-            if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = sum;
-            __syncthreads();
-            if (threadIdx.x == 0) {
-                float total = part[0];
-#pragma unroll
-                for (int i = 1; i < kGradThreads / 64; ++i) total += part[i];
-                dw[t * K + j] = ok ? total : 0.0f;
+            const int j = threadIdx.x;
+            if (j < KG && j0 + j < K) {
+                float total = part[0][j];
+                for (int i = 1; i < static_cast<int>(blockDim.x >> 6); ++i) total += part[i][j];
+                dw[t * K + j0 + j] = slot_ok(slot[t * K + j0 + j], num_rows) ? total : 0.0f;
             }
         }
     }
@@ -406,8 +431,16 @@ hipError_t launch_combine(const CopyParams &c, const uint16_t *y, const int32_t 
 
 hipError_t launch_combine_backward(const CopyParams &c, const uint16_t *dout, const uint16_t *y, const int32_t *slot,
                                    const float *w, uint16_t *dy, float *dw, hipStream_t stream) {
-    const dim3 grid(c.T, c.K);
-    combine_backward_kernel<<<grid, kGradThreads, 0, stream>>>(dout, y, slot, w, dy, dw, c.H, c.K, c.nvec, 1, c.num_rows);
+    const bool few = c.T < kGradTokens;
+    // two vectors a thread, or one for rows of less than that
+    const int want = (c.nvec + 1) / 2, threads = min(kGradMaxThreads, (want + 63) / 64 * 64);
+    const dim3 grid(c.T, few ? c.K : 1);
+    if (few || c.K == 1)
+        combine_backward_kernel<1><<<grid, threads, 0, stream>>>(dout, y, slot, w, dy, dw, c.H, c.K, c.nvec, c.num_rows);
+    else if (c.K <= 4)
+        combine_backward_kernel<4><<<grid, threads, 0, stream>>>(dout, y, slot, w, dy, dw, c.H, c.K, c.nvec, c.num_rows);
+    else
+        combine_backward_kernel<8><<<grid, threads, 0, stream>>>(dout, y, slot, w, dy, dw, c.H, c.K, c.nvec, c.num_rows);
     return hipGetLastError();
 }
 
