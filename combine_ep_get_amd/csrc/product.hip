@@ -605,7 +605,7 @@ hipError_t launch_tiled(const Args &a, hipStream_t stream) {
 template <int MODE, int ACT, bool FP8, class Args>
 hipError_t launch_sized(const Args &a, hipStream_t stream) {
     if constexpr (FP8) {
-        return launch_tiled<MODE, ACT, true, 4, 2, 4, 4>(a, stream);
+        return launch_tiled<MODE, ACT, true, 2, 2, 4, 4>(a, stream);
     } else {
         if (a.mean_rows >= (MODE == kForward ? 160 : 64)) return launch_tiled<MODE, ACT, false, 2, 4, 8, 4>(a, stream);
         return launch_tiled<MODE, ACT, false, 2, 2, 4, 4>(a, stream);
