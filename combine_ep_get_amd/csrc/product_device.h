@@ -47,12 +47,16 @@ __device__ __forceinline__ float act_slope(float v) {
     return 1.0f;
 }
 
+__device__ __forceinline__ u32x4 pack_bf16(const f32x4 (&v)[2]) {
+    return u32x4{pack_bf16x2(v[0][0], v[0][1]), pack_bf16x2(v[0][2], v[0][3]), pack_bf16x2(v[1][0], v[1][1]),
+                 pack_bf16x2(v[1][2], v[1][3])};
+}
+
 // bf16 of 4 G neighbouring values, and back.
 template <int G>
 __device__ __forceinline__ void store_bf16(uint16_t *p, const f32x4 (&v)[G]) {
     if constexpr (G == 2)
-        *reinterpret_cast<u32x4 *>(p) = u32x4{pack_bf16x2(v[0][0], v[0][1]), pack_bf16x2(v[0][2], v[0][3]),
-                                              pack_bf16x2(v[1][0], v[1][1]), pack_bf16x2(v[1][2], v[1][3])};
+        *reinterpret_cast<u32x4 *>(p) = pack_bf16(v);
     else
         *reinterpret_cast<u32x2 *>(p) = u32x2{pack_bf16x2(v[0][0], v[0][1]), pack_bf16x2(v[0][2], v[0][3])};
 }
