@@ -183,7 +183,7 @@ __device__ __forceinline__ void accumulate_fewer(int live, F &f) {
 }
 
 template <int MODE, int ACT, bool FP8, int WF, int WT, int FF, int TF, class Args>
-__global__ __launch_bounds__(64 * WF * WT) void product_kernel(Args a) {
+__global__ __launch_bounds__(64 * WF * WT, 2) void product_kernel(Args a) {
     constexpr int NT = 64 * WF * WT, NW = WF * WT;
     constexpr int BF = WF * FF * 16, BT = WT * TF * 16;
     constexpr bool kPs = MODE != kForward, kQs = MODE == kGradWeight;
@@ -300,12 +300,31 @@ __global__ __launch_bounds__(64 * WF * WT) void product_kernel(Args a) {
         struct Scales {
             float x[TF], w[2];
         } sa, sb;
+        // The tokens' scales come four blocks at a time, a lane of each token
+        // one of them (with a load a block, the lines that they lie in made half of the L2's
+        // requests); a step takes its block's by permuting the lanes.
+        float sx[TF], sx_next[TF];
+        auto load_scales = [&](int s) {
+            if constexpr (FP8) {
+                const int at = min(s + (fresh_lane() >> 4), a.C / 128 - 1);
+#pragma unroll
+                for (int t = 0; t < TF; ++t) sx_next[t] = sf_row[t][at * a.sf_hs];
+            }
+        };
         auto read_scales = [&](Scales &to, int s) {
             if constexpr (FP8) {
+                if ((s & 3) == 0) {
 #pragma unroll
-                for (int t = 0; t < TF; ++t) to.x[t] = sf_row[t][s * a.sf_hs];
-                to.w[0] = sf_w[0][s];
-                to.w[1] = sf_w[1][s];
+                    for (int t = 0; t < TF; ++t) sx[t] = sx_next[t];
+                    load_scales(s + 4);
+                }
+                const int from = ((fresh_lane() & 15) + 16 * (s & 3)) * 4;
+#pragma unroll
+                for (int t = 0; t < TF; ++t)
+                    to.x[t] = __int_as_float(__builtin_amdgcn_ds_bpermute(from, __float_as_int(sx[t])));
+                typedef const __attribute__((address_space(4))) float *constant;  // read by the scalar unit
+                to.w[0] = ((constant)sf_w[0])[s];
+                to.w[1] = ((constant)sf_w[1])[s];
             }
         };
 
@@ -425,6 +444,7 @@ __global__ __launch_bounds__(64 * WF * WT) void product_kernel(Args a) {
                     fetch(pl, ql);
                 }
             };
+            load_scales(0);
             if (pad) {
                 if constexpr (FP8) {
 #pragma unroll
@@ -437,8 +457,8 @@ __global__ __launch_bounds__(64 * WF * WT) void product_kernel(Args a) {
                 __syncthreads();
             } else {
                 first_step(p0, q0);
-                read_scales(sa, 0);
                 wait_loads_and_sync();
+                read_scales(sa, 0);
                 fetch(p1, q1);
             }
             read_q(qa, q0, 0);
