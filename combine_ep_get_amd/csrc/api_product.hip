@@ -31,6 +31,8 @@ int check_product(const ep_product *q, int32_t multiple) {
     for (int32_t n : {q->in_features, q->out_features})
         if (n < 8 || n % multiple != 0 || n > EP_MAX_FEATURES) return EP_ERR_INVALID_ARG;
     if (q->activation < EP_ACT_NONE || q->activation > EP_ACT_GEGLU) return EP_ERR_INVALID_ARG;
+    // the kernels reach into an expert's weight with 32-bit byte offsets
+    if (static_cast<int64_t>(weight_rows(q)) * q->in_features > EP_MAX_WEIGHT) return EP_ERR_INVALID_ARG;
     return EP_OK;
 }
 

@@ -84,6 +84,8 @@ extern "C" {
 
 /* Largest in_features and out_features of an expert product. */
 #define EP_MAX_FEATURES (1 << 16)
+/* Largest number of values of one expert's weight (a 4 GiB bf16 matrix). */
+#define EP_MAX_WEIGHT (INT64_C(1) << 31)
 /* Largest num_tokens of ep_moe_tokens and ep_moe_tokens_fp8. */
 #define EP_MOE_TOKENS_MAX 128
 
@@ -112,7 +114,8 @@ typedef struct ep_problem {
 
 /* One product of every expert.  C and N are multiples of 8 in
  * [8, EP_MAX_FEATURES]; the expert's weight has M rows of C values: M = N,
- * or 2N with a gated activation (the gates' rows first). */
+ * or 2N with a gated activation (the gates' rows first), and M * C <=
+ * EP_MAX_WEIGHT. */
 typedef struct ep_product {
     int32_t in_features;  /* C */
     int32_t out_features; /* N */
@@ -419,8 +422,9 @@ int ep_combine_backward(const ep_problem *problem, const uint16_t *dout, const u
  *   residual      [R*S,N] bf16 device, or NULL; may be out
  *   pre           [R*S,M] bf16 device, or NULL: v, rounded, for the backward pass
  *   out           [R*S,N] bf16 device
- * All of x, weight, bias, residual, pre and out are 16-byte aligned.  The
- * result of a row does not depend on the other rows' values. */
+ * All of x, weight, bias, residual, pre and out are 16-byte aligned, and but
+ * for residual and out no output overlaps another array.  The result of a
+ * row does not depend on the other rows' values. */
 int ep_expert_product(const ep_problem *problem, const ep_product *product, const uint16_t *x,
                       const int32_t *expert_count, const int32_t *expert_offset,
                       const uint16_t *weight, const float *bias, const uint16_t *residual,
@@ -467,8 +471,9 @@ size_t ep_product_workspace_bytes(const ep_problem *problem, const ep_product *p
  *               rows), or NULL
  *   dweight_acc [E,M,C] fp32 device, added to, or NULL
  *   dbias       [E,M] fp32 device, overwritten, or NULL
- *   workspace   ep_product_workspace_bytes bytes, 256-byte aligned; NULL
- *               (with 0 bytes) without dbias
+ *   workspace   ep_product_workspace_bytes bytes, 256-byte aligned; calls
+ *               that may overlap need one each; NULL (with 0 bytes) without
+ *               dbias
  * bf16 and fp32 arrays are 16-byte aligned. */
 int ep_expert_product_backward(const ep_problem *problem, const ep_product *product,
                                const uint16_t *dout, const uint16_t *pre, const uint16_t *x,

@@ -65,6 +65,9 @@ CASES = [
     (700, 256, 520, 4, 2, 2, 1, "geglu", True, True, True),
     (1100, 328, 392, 2, 2, 1, 1, "silu", True, True, True),
     (600, 64, 264, 1, 1, 1, 1, "swiglu", False, False, True),
+    (9, 264, 1000, 3, 1, 1, 1, "gelu", True, True, False),     # few rows, several tiles of outputs
+    (150, 1032, 72, 2, 1, 2, 1, "relu", False, False, True),   # an odd number of steps and a part step
+    (4000, 72, 8200, 16, 2, 4, 1, "none", False, False, False),  # more tiles than workgroups
 ]
 
 
@@ -165,12 +168,32 @@ def test_values_that_are_not_finite_stay_in_their_row(ep, T):
     assert untouched(out, used)
 
 
+def test_rows_past_32_bits(ep):
+    """A slice that starts past 4 GiB of x and out."""
+    C, N, S = 16384, 8192, 300_000
+    r = Routed(ep, 6, 2, 1, R=2, S=S)
+    assert max(r.used) >= S
+    q = ep.Product.make(C, N)
+    g = torch.Generator().manual_seed(0)
+    x = torch.empty(r.rows, C, dtype=torch.bfloat16, device="cuda")
+    rows = torch.tensor(r.used)
+    xs, w = normal(g, len(r.used), C), normal(g, 2, N, C, scale=C ** -0.5)
+    x[rows.cuda()] = xs.cuda()
+    out = torch.empty(r.rows, N, dtype=torch.bfloat16, device="cuda")
+    ep.ep_expert_product(r.p, q, x, *r.arrays, w.cuda(), None, None, None, out)
+    for e, of in r.of.items():
+        o, b, _, _ = ref.product("none", xs[[r.used.index(i) for i in of]], w[e])
+        ref.assert_within(out[of], o, b)
+
+
 FP8_CASES = [
     (1, 128, 128, 4, 2, 1, "swiglu", "token", False, False),
     (30, 256, 384, 8, 2, 2, "none", "padded", True, True),
     (200, 640, 256, 4, 2, 2, "swiglu", "column", True, False),
     (700, 384, 512, 3, 2, 1, "geglu", "token", False, True),
     (513, 256, 128, 1, 1, 1, "silu", "column", True, True),
+    (260, 1152, 128, 2, 2, 1, "none", "padded", False, False),
+    (90, 1664, 256, 2, 1, 1, "geglu", "column", True, False),
 ]
 
 

@@ -64,6 +64,8 @@ def test_bad_problems_and_products(fn):
     for bad in (Q(C=0), Q(C=252), Q(N=4), Q(N=130), Q(C=(1 << 16) + 128), Q(N=(1 << 16) + 128), Q(act=-1), Q(act=6),
                 Q(reserved=1)):
         assert fn(q=bad) == BAD, (bad.in_features, bad.out_features, bad.activation)
+    # a weight of more than 2^31 values: 32768 outputs, both halves of a gate
+    assert fn(q=Q(C=32768 + 128, N=32768), p=P(H=32768 + 128)) == BAD
     assert ep.load().ep_expert_product(ctypes.byref(P()), None, A, A, A, A, A, A, A, A, None) == BAD
 
 
@@ -112,6 +114,8 @@ def test_backward_combinations():
     assert backward(q=none, pre=None, dpre=A) == BAD
     need = ep.ep_product_workspace_bytes(P(), Q())
     assert need > 0 and backward(n=need - 1) == BAD
+    assert ep.ep_product_workspace_bytes(P(), Q(C=32768, N=32768)) > 0       # 2^31 values exactly
+    assert ep.ep_product_workspace_bytes(P(), Q(C=32768, N=32768 + 8)) == 0
     assert ep.ep_product_workspace_bytes(P(), Q(C=4)) == 0 and ep.ep_product_workspace_bytes(P(S=0), Q()) == 0
 
 
