@@ -6,7 +6,8 @@
 // rows when gated), its waves the blocks of k in turn; the sums are joined in
 // LDS in a fixed order.  A tile of the tiled product would spend its LDS traffic and
 // barriers on rows that are not there, and its grid of 128 outputs a
-// workgroup leaves most of the chip idle on one small product.
+// workgroup leaves most of the chip idle on one small product.  With
+// kWaveItems tiles or more each wave takes tiles of its own, over all of k.
 #include <type_traits>
 
 #include "few_device.h"
@@ -33,8 +34,10 @@ __global__ __launch_bounds__(kFewThreads) void product_few_kernel(ProductArgs a)
     const int nf = (a.N + 15) / 16;
     const int64_t total = static_cast<int64_t>(first[a.seg.E]) * nf;
     const int64_t pitch = static_cast<int64_t>(a.C) * (FP8 ? 1 : 2);
-    for (int64_t round = 0; round * gridDim.x < total; ++round) {
-        const int64_t tile = tile_of(total, round, blockIdx.x, gridDim.x);
+    const bool alone = total >= kWaveItems;
+    const int G = gridDim.x * (alone ? kFewWaves : 1), worker = blockIdx.x + (alone ? wave * gridDim.x : 0);
+    for (int64_t round = 0; round * G < total; ++round) {
+        const int64_t tile = tile_of(total, round, worker, G);
         if (tile < 0) break;
         const int e = tile_expert(first, a.seg.E, static_cast<int>(tile / nf));
         const int f0 = __builtin_amdgcn_readfirstlane(first[e]);
@@ -63,7 +66,17 @@ __global__ __launch_bounds__(kFewThreads) void product_few_kernel(ProductArgs a)
         }
         // neighbouring tiles start at different blocks of k, so that they do
         // not all read the same piece of x at once (1.5 us of 14)
-        accumulate_blocks<FP8, FP8>(acc, row, col, w_sf, x_sf, a.sf_hs, a.C, (wave + ft) % kFewWaves, kFewWaves, lg);
+        accumulate_blocks<FP8, FP8>(acc, row, col, w_sf, x_sf, a.sf_hs, a.C, alone ? 0 : (wave + ft) % kFewWaves,
+                                    alone ? 1 : kFewWaves, lg);
+        if (alone) {
+#pragma unroll
+            for (int t = 0; t < TF; ++t) {
+                const int tok = t0 + t * 16 + li, n = n0 + lg * 4;
+                f32x4 v[1] = {acc[0][t]}, u[1] = {acc[FF - 1][t]};
+                if (tok < rows && n < a.N) write_outputs<ACT>(a, e, row0 + tok, n, v, u);
+            }
+            continue;
+        }
 #pragma unroll
         for (int f = 0; f < FF; ++f)
 #pragma unroll
@@ -85,7 +98,7 @@ template <int ACT, bool FP8, int TF>
 hipError_t launch_few(const ProductArgs &a, hipStream_t stream) {
     // no more workgroups than tiles there can be, each expert's last tile in part filled
     const int64_t tiles = (a.entries / (16 * TF) + min(static_cast<int64_t>(a.seg.E), a.entries)) * ((a.N + 15) / 16);
-    const uint32_t grid = static_cast<uint32_t>(min(int64_t{1024}, (tiles + 7) / 8 * 8));
+    const uint32_t grid = static_cast<uint32_t>(min(int64_t{512}, (tiles + 7) / 8 * 8));
     product_few_kernel<ACT, FP8, TF><<<grid, kFewThreads, 0, stream>>>(a);
     return hipGetLastError();
 }

@@ -87,8 +87,7 @@ __device__ __forceinline__ void sort_entries(const TokensArgs &a, EntryLists &l)
 // up: items are (expert with entries, 16 outputs).  With enough items for
 // every wave of the chip, a wave takes an item by itself and waits for no
 // other; else a workgroup does, each wave a share of k, joined in LDS.
-// kWaveItems: items from which waves work alone (8 waves on each of 256 CUs).
-constexpr int kWaveItems = 2048;
+constexpr int kTokenCUs = 256;
 
 // This lane's sums of columns c0 .. c0 + 16 CF - 1 of expert e's entries and
 // outputs n0 .. n0 + 15 (of both halves when gated) over a share of k.
@@ -219,8 +218,10 @@ __device__ __forceinline__ void down_columns(const TokensArgs &a, const EntryLis
     }
 }
 
-template <bool FP8, int FF>
-__global__ __launch_bounds__(kFewThreads) void tokens_down_kernel(TokensArgs a) {
+// MANY: an expert may have more than 16 entries, for which the code takes the registers of
+// a second workgroup on the CU.
+template <bool FP8, int FF, bool MANY>
+__global__ __launch_bounds__(kFewThreads, MANY ? 2 : 4) void tokens_down_kernel(TokensArgs a) {
     __shared__ EntryLists l;
     extern __shared__ __attribute__((aligned(16))) float sums[];
     sort_entries(a, l);
@@ -234,7 +235,7 @@ __global__ __launch_bounds__(kFewThreads) void tokens_down_kernel(TokensArgs a) 
         const int e = __builtin_amdgcn_readfirstlane(l.expert[u / shares]);
         const int s0 = __builtin_amdgcn_readfirstlane(l.start(e)), m = __builtin_amdgcn_readfirstlane(l.end[e]) - s0;
         for (int c0 = 0; c0 < m; c0 += 32) {
-            if (m - c0 <= 16)
+            if (!MANY || m - c0 <= 16)
                 down_columns<FP8, FF, 1>(a, l, mine, e, c0, m, s0, n0, u % shares, shares);
             else
                 down_columns<FP8, FF, 2>(a, l, mine, e, c0, m, s0, n0, u % shares, shares);
@@ -267,7 +268,8 @@ template <bool FP8>
 hipError_t launch_up(const TokensArgs &a, hipStream_t stream) {
     const int64_t entries = static_cast<int64_t>(a.T) * a.K;
     const int64_t items = (entries < a.E ? entries : a.E) * ((a.I + 15) / 16);
-    const uint32_t grid = static_cast<uint32_t>(items < 1 ? 1 : items < 1024 ? items : 1024);
+    // one workgroup fits a CU's registers: no more, so that each sorts the entries once
+    const uint32_t grid = static_cast<uint32_t>(items < 1 ? 1 : items < kTokenCUs ? items : kTokenCUs);
     switch (a.act) {
 #define EP_ACT_CASE(A) \
     case A: tokens_up_kernel<A, FP8><<<grid, kFewThreads, 0, stream>>>(a); break;
@@ -285,14 +287,16 @@ hipError_t launch_up(const TokensArgs &a, hipStream_t stream) {
 
 template <bool FP8>
 hipError_t launch_down(const TokensArgs &a, hipStream_t stream) {
-    // 32 outputs a workgroup where the tokens' sums fill most of a CU's LDS
-    // anyway, else 16, of which two or more run on a CU
-    const int ff = a.T > 64 ? 2 : 1;
+    // 32 outputs a workgroup where the tokens' sums leave a CU's LDS to one
+    // workgroup anyway and there are enough of them, else 16
+    const int ff = a.T > 64 && a.H >= 4096 ? 2 : 1;
     const uint32_t grid = (a.H + 16 * ff - 1) / (16 * ff), lds = kFewWaves * a.T * 16 * ff * 4;
     if (ff == 2)
-        tokens_down_kernel<FP8, 2><<<grid, kFewThreads, lds, stream>>>(a);
+        tokens_down_kernel<FP8, 2, true><<<grid, kFewThreads, lds, stream>>>(a);
+    else if (a.T > 16)
+        tokens_down_kernel<FP8, 1, true><<<grid, kFewThreads, lds, stream>>>(a);
     else
-        tokens_down_kernel<FP8, 1><<<grid, kFewThreads, lds, stream>>>(a);
+        tokens_down_kernel<FP8, 1, false><<<grid, kFewThreads, lds, stream>>>(a);
     return hipGetLastError();
 }
 
