@@ -2,7 +2,7 @@
 //
 //   out[r,n] = act(sum_c x[r,c] W[e,n,c] + b[e,n]) + residual[r,n]
 //
-// One workgroup takes up to 16 TF rows of an expert and 16 outputs (32 weight
+// One workgroup takes up to 16 rows of an expert and 16 outputs (32 weight
 // rows when gated), its waves the blocks of k in turn; the sums are joined in
 // LDS in a fixed order.  A tile of the tiled product would spend its LDS traffic and
 // barriers on rows that are not there, and its grid of 128 outputs a
@@ -15,18 +15,18 @@
 namespace epget {
 namespace {
 
-template <int ACT, bool FP8, int TF>
+template <int ACT, bool FP8>
 __global__ __launch_bounds__(kFewThreads) void product_few_kernel(ProductArgs a) {
     constexpr bool GATED = act_gated(ACT);
     constexpr int FF = GATED ? 2 : 1;
     __shared__ int first[EP_MAX_EXPERTS + 1];
     __shared__ int wave_sum[kFewWaves];
-    __shared__ f32x4 part[kFewWaves][FF][TF][64];
+    __shared__ f32x4 part[kFewWaves][FF][64];
     if (a.seg.E > 1) {
-        tile_prefix<kFewThreads>(a.seg, 16 * TF, first, wave_sum);
+        tile_prefix<kFewThreads>(a.seg, 16, first, wave_sum);
     } else if (threadIdx.x < 2) {  // no sums over experts: a decode-sized product is mostly latency
         int64_t row0;
-        first[threadIdx.x] = threadIdx.x ? (segment(a.seg, 0, &row0) + 16 * TF - 1) / (16 * TF) : 0;
+        first[threadIdx.x] = threadIdx.x ? (segment(a.seg, 0, &row0) + 15) / 16 : 0;
     }
     __syncthreads();
     const int lane = __lane_id(), li = lane & 15, lg = lane >> 4;
@@ -46,67 +46,50 @@ __global__ __launch_bounds__(kFewThreads) void product_few_kernel(ProductArgs a)
         tile_in_expert(tile - static_cast<int64_t>(f0) * nf, nt, nf, &tt, &ft);
         int64_t row0;
         const int rows = segment(a.seg, e, &row0);
-        const int n0 = ft * 16, t0 = tt * 16 * TF;
-        const char *row[FF], *col[TF];
-        const float *w_sf[FF], *x_sf[TF];
+        const int n0 = ft * 16, t0 = tt * 16;
+        const char *row[FF];
+        const float *w_sf[FF];
+        f32x4 acc[FF][1];
 #pragma unroll
         for (int f = 0; f < FF; ++f) {
             const int64_t r = static_cast<int64_t>(e) * a.M + f * a.N + min(n0 + li, a.N - 1);
             row[f] = static_cast<const char *>(a.weight) + r * pitch;
             w_sf[f] = FP8 ? a.w_sf + (static_cast<int64_t>(e) * (a.M / 128) + (f * a.N + n0) / 128) * (a.C / 128) : nullptr;
+            acc[f][0] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
         }
-        f32x4 acc[FF][TF];
-#pragma unroll
-        for (int t = 0; t < TF; ++t) {
-            const int64_t r = row0 + min(t0 + t * 16 + li, rows - 1);
-            col[t] = static_cast<const char *>(a.x) + r * pitch;
-            x_sf[t] = FP8 ? a.x_sf + r * a.sf_ts : nullptr;
-#pragma unroll
-            for (int f = 0; f < FF; ++f) acc[f][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-        }
+        const int64_t xr = row0 + min(t0 + li, rows - 1);
+        const char *const col[1] = {static_cast<const char *>(a.x) + xr * pitch};
+        const float *const x_sf[1] = {FP8 ? a.x_sf + xr * a.sf_ts : nullptr};
         // neighbouring tiles start at different blocks of k, so that they do
         // not all read the same piece of x at once (1.5 us of 14)
         accumulate_blocks<FP8, FP8>(acc, row, col, w_sf, x_sf, a.sf_hs, a.C, alone ? 0 : (wave + ft) % kFewWaves,
                                     alone ? 1 : kFewWaves, lg);
+        const int tok = t0 + li, n = n0 + lg * 4;
+        const bool mine = tok < rows && n < a.N;
         if (alone) {
-#pragma unroll
-            for (int t = 0; t < TF; ++t) {
-                const int tok = t0 + t * 16 + li, n = n0 + lg * 4;
-                f32x4 v[1] = {acc[0][t]}, u[1] = {acc[FF - 1][t]};
-                if (tok < rows && n < a.N) write_outputs<ACT>(a, e, row0 + tok, n, v, u);
-            }
+            f32x4 v[1] = {acc[0][0]}, u[1] = {acc[FF - 1][0]};
+            if (mine) write_outputs<ACT>(a, e, row0 + tok, n, v, u);
             continue;
         }
 #pragma unroll
-        for (int f = 0; f < FF; ++f)
-#pragma unroll
-            for (int t = 0; t < TF; ++t) part[wave][f][t][lane] = acc[f][t];
+        for (int f = 0; f < FF; ++f) part[wave][f][lane] = acc[f][0];
         __syncthreads();
-        // wave t joins and writes fragment t
-        for (int t = wave; t < TF; t += kFewWaves) {
-            const int tok = t0 + t * 16 + li, n = n0 + lg * 4;
-            if (tok >= rows || n >= a.N) continue;
-            f32x4 v[1] = {sum_waves(&part[0][0][t][lane], FF * TF * 64)};
-            f32x4 u[1] = {GATED ? sum_waves(&part[0][FF - 1][t][lane], FF * TF * 64) : v[0]};
+        if (wave == 0 && mine) {
+            f32x4 v[1] = {sum_waves(&part[0][0][lane], FF * 64)};
+            f32x4 u[1] = {GATED ? sum_waves(&part[0][FF - 1][lane], FF * 64) : v[0]};
             write_outputs<ACT>(a, e, row0 + tok, n, v, u);
         }
         __syncthreads();
     }
 }
 
-template <int ACT, bool FP8, int TF>
-hipError_t launch_few(const ProductArgs &a, hipStream_t stream) {
-    // no more workgroups than tiles there can be, each expert's last tile in part filled
-    const int64_t tiles = (a.entries / (16 * TF) + min(static_cast<int64_t>(a.seg.E), a.entries)) * ((a.N + 15) / 16);
-    const uint32_t grid = static_cast<uint32_t>(min(int64_t{512}, (tiles + 7) / 8 * 8));
-    product_few_kernel<ACT, FP8, TF><<<grid, kFewThreads, 0, stream>>>(a);
-    return hipGetLastError();
-}
-
 template <int ACT, bool FP8>
 hipError_t launch_few(const ProductArgs &a, hipStream_t stream) {
-    if (a.entries <= 16 * a.seg.E) return launch_few<ACT, FP8, 1>(a, stream);
-    return launch_few<ACT, FP8, 3>(a, stream);
+    // no more workgroups than tiles there can be, each expert's last tile in part filled
+    const int64_t tiles = (a.entries / 16 + min(static_cast<int64_t>(a.seg.E), a.entries)) * ((a.N + 15) / 16);
+    const uint32_t grid = static_cast<uint32_t>(min(int64_t{512}, (tiles + 7) / 8 * 8));
+    product_few_kernel<ACT, FP8><<<grid, kFewThreads, 0, stream>>>(a);
+    return hipGetLastError();
 }
 
 }  // namespace

@@ -339,147 +339,148 @@ __global__ __launch_bounds__(64 * WF * WT, 2) void product_kernel(Args a) {
 
         const int lane = fresh_lane();
         auto accumulate = [&](auto live_fragments) {
-        constexpr int TA = live_fragments();
-        // A step is computed in phases of half of P's fragments, each with 32
-        // k (bf16: four phases) or all 128 k (FP8: two).  Each phase's
-        // fragments are read from LDS while the phase before it multiplies.
-        constexpr int PF = FF / 2, KS = FP8 ? 2 : 1;
-        union Frag {
-            bf16x8 part[KS];
-            i32x8 all;  // FP8
-        };
-        struct PFrags {
-            Frag f[PF];
-        } pa, pb;
-        struct QFrags {
-            Frag t[TF];
-        } qa, qb;
-        auto read_p = [&](PFrags &h, const char *pl, int ks, int half) {
+            constexpr int TA = live_fragments();
+            // A step is computed in phases of half of P's fragments, each with 32
+            // k (bf16: four phases) or all 128 k (FP8: two).  Each phase's
+            // fragments are read from LDS while the phase before it multiplies.
+            constexpr int PF = FF / 2, KS = FP8 ? 2 : 1;
+            union Frag {
+                bf16x8 part[KS];
+                i32x8 all;  // FP8
+            };
+            struct PFrags {
+                Frag f[PF];
+            } pa, pb;
+            struct QFrags {
+                Frag t[TF];
+            } qa, qb;
+            auto read_p = [&](PFrags &h, const char *pl, int ks, int half) {
 #pragma unroll
-            for (int f = 0; f < PF; f += 2)
+                for (int f = 0; f < PF; f += 2)
 #pragma unroll
-                for (int k = 0; k < KS; ++k)
-                    Tile<BF, kPs, true>::pair(pl, lane, wf * FF + half * PF + f, FP8 ? k : ks, h.f[f].part[k],
-                                              h.f[f + 1].part[k]);
-        };
-        auto read_q = [&](QFrags &h, const char *ql, int ks) {
+                    for (int k = 0; k < KS; ++k)
+                        Tile<BF, kPs, true>::pair(pl, lane, wf * FF + half * PF + f, FP8 ? k : ks, h.f[f].part[k],
+                                                  h.f[f + 1].part[k]);
+            };
+            auto read_q = [&](QFrags &h, const char *ql, int ks) {
 #pragma unroll
-            for (int t = 0; t < TA; ++t)
+                for (int t = 0; t < TA; ++t)
 #pragma unroll
-                for (int k = 0; k < KS; ++k) h.t[t].part[k] = Tile<BT, kQs, false>::fragment(ql, lane, wt * TA + t, FP8 ? k : ks);
-        };
-        auto multiply = [&](const PFrags &pf, const QFrags &qf, const Scales &sc, int half) {
-            if constexpr (FP8) {
-                // A block's products are scaled in fp32 while the matrix unit
-                // does the next fragment's: left to itself, the compiler waits for
-                // each product and scales it at once.
-                f32x4 d[2][TA];
+                    for (int k = 0; k < KS; ++k)
+                        h.t[t].part[k] = Tile<BT, kQs, false>::fragment(ql, lane, wt * TA + t, FP8 ? k : ks);
+            };
+            auto multiply = [&](const PFrags &pf, const QFrags &qf, const Scales &sc, int half) {
+                if constexpr (FP8) {
+                    // A block's products are scaled in fp32 while the matrix unit
+                    // does the next fragment's: left to itself, the compiler waits for
+                    // each product and scales it at once.
+                    f32x4 d[2][TA];
 #pragma unroll
-                for (int f = 0; f <= PF; ++f) {
+                    for (int f = 0; f <= PF; ++f) {
 #pragma unroll
-                    for (int t = 0; t < TA; ++t) {
-                        const f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
-                        if (f < PF)  // block scales of one (127 is 2^0)
-                            d[f & 1][t] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                                pf.f[f].all, qf.t[t].all, zero, 0, 0, 0, 0x7F7F7F7F, 0, 0x7F7F7F7F);
-                        if (f > 0) {
-                            const float scale = sc.x[t] * sc.w[GATED ? (f - 1) & 1 : 0];
-                            f32x4 &to = acc[half * PF + f - 1][t];
+                        for (int t = 0; t < TA; ++t) {
+                            const f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
+                            if (f < PF)  // block scales of one (127 is 2^0)
+                                d[f & 1][t] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                                    pf.f[f].all, qf.t[t].all, zero, 0, 0, 0, 0x7F7F7F7F, 0, 0x7F7F7F7F);
+                            if (f > 0) {
+                                const float scale = sc.x[t] * sc.w[GATED ? (f - 1) & 1 : 0];
+                                f32x4 &to = acc[half * PF + f - 1][t];
 #pragma unroll
-                            for (int r = 0; r < 4; ++r) to[r] = __builtin_fmaf(d[(f - 1) & 1][t][r], scale, to[r]);
-                            __builtin_amdgcn_sched_barrier(0);
+                                for (int r = 0; r < 4; ++r) to[r] = __builtin_fmaf(d[(f - 1) & 1][t][r], scale, to[r]);
+                                __builtin_amdgcn_sched_barrier(0);
+                            }
                         }
+                        __builtin_amdgcn_sched_barrier(0);
                     }
-                    __builtin_amdgcn_sched_barrier(0);
-                }
-            } else {
-#pragma unroll
-                for (int f = 0; f < PF; ++f)
-#pragma unroll
-                    for (int t = 0; t < TA; ++t)
-                        acc[half * PF + f][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                            pf.f[f].part[0], qf.t[t].part[0], acc[half * PF + f][t], 0, 0, 0);
-                __builtin_amdgcn_sched_barrier(0);  // phases stay apart: 16 % slower without
-            }
-        };
-
-        // A part step comes first, if k is no multiple of the step.
-        constexpr int kUnit = MODE == kGradWeight ? kStepRows : kStepBytes;
-        const int full = static_cast<int>(k_total / kUnit);
-        const int left = static_cast<int>(k_total - static_cast<int64_t>(full) * kUnit);
-        // The loop takes two steps a round, one a buffer: an odd number of
-        // steps has one of zeros before it, whose products pass while the
-        // first loads are on their way.
-        const int steps = full + (left > 0), pad = steps & 1, total_steps = steps + pad;
-        auto fetch = [&](char *pl, char *ql) {
-            p.load(pl);
-            // the loads of the live rows: 8 a wave and load
-            q.template load<kQs ? q.kLoads : (WT * TA * 2 + NW - 1) / NW>(ql);
-        };
-        // One step, with Q's first fragments in q0f: when every wave has read
-        // all of this buffer and the next step's loads have landed, the loads
-        // of the step after that start into this buffer, and the next step's
-        // first fragments are read into q1f (FP8) or q0f during the last phase.
-        auto step = [&](char *pl, char *ql, char *pn, char *qn, QFrags &q0f, QFrags &q1f, const Scales &sc, Scales &next,
-                        int s, auto fetch_more, auto more) {
-            if constexpr (more()) read_scales(next, s + 1 - pad);  // waited for with the loads to LDS
-            read_p(pb, pl, 0, 1);
-            multiply(pa, q0f, sc, 0);
-            if constexpr (!FP8) {
-                read_q(q1f, ql, 1);
-                read_p(pa, pl, 1, 0);
-                multiply(pb, q0f, sc, 1);
-                read_p(pb, pl, 1, 1);
-                multiply(pa, q1f, sc, 0);
-            }
-            if constexpr (more()) {
-                wait_loads_and_sync();
-                if constexpr (fetch_more()) fetch(pl, ql);
-                read_q(FP8 ? q1f : q0f, qn, 0);
-                read_p(pa, pn, 0, 0);
-            }
-            multiply(pb, FP8 ? q0f : q1f, sc, 1);
-        };
-        constexpr std::true_type yes{};
-        constexpr std::false_type no{};
-        if (total_steps > 0) {
-            __syncthreads();  // the previous tile's readers are done
-            auto first_step = [&](char *pl, char *ql) {
-                if (left > 0) {
-                    // k of grad input is bytes of dpre, rows of the weight
-                    p.load_part(pl, MODE == kGradInput ? left / 2 : left);
-                    q.load_part(ql, left);
                 } else {
-                    fetch(pl, ql);
+#pragma unroll
+                    for (int f = 0; f < PF; ++f)
+#pragma unroll
+                        for (int t = 0; t < TA; ++t)
+                            acc[half * PF + f][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                                pf.f[f].part[0], qf.t[t].part[0], acc[half * PF + f][t], 0, 0, 0);
+                    __builtin_amdgcn_sched_barrier(0);  // phases stay apart: 16 % slower without
                 }
             };
-            load_scales(0);
-            if (pad) {
-                if constexpr (FP8) {
-#pragma unroll
-                    for (int t = 0; t < TF; ++t) sa.x[t] = 0.0f;
-                    sa.w[0] = sa.w[1] = 0.0f;
+
+            // A part step comes first, if k is no multiple of the step.
+            constexpr int kUnit = MODE == kGradWeight ? kStepRows : kStepBytes;
+            const int full = static_cast<int>(k_total / kUnit);
+            const int left = static_cast<int>(k_total - static_cast<int64_t>(full) * kUnit);
+            // The loop takes two steps a round, one a buffer: an odd number of
+            // steps has one of zeros before it, whose products pass while the
+            // first loads are on their way.
+            const int steps = full + (left > 0), pad = steps & 1, total_steps = steps + pad;
+            auto fetch = [&](char *pl, char *ql) {
+                p.load(pl);
+                // the loads of the live rows: 8 a wave and load
+                q.template load<kQs ? q.kLoads : (WT * TA * 2 + NW - 1) / NW>(ql);
+            };
+            // One step, with Q's first fragments in q0f: when every wave has read
+            // all of this buffer and the next step's loads have landed, the loads
+            // of the step after that start into this buffer, and the next step's
+            // first fragments are read into q1f (FP8) or q0f during the last phase.
+            auto step = [&](char *pl, char *ql, char *pn, char *qn, QFrags &q0f, QFrags &q1f, const Scales &sc, Scales &next,
+                            int s, auto fetch_more, auto more) {
+                if constexpr (more()) read_scales(next, s + 1 - pad);  // waited for with the loads to LDS
+                read_p(pb, pl, 0, 1);
+                multiply(pa, q0f, sc, 0);
+                if constexpr (!FP8) {
+                    read_q(q1f, ql, 1);
+                    read_p(pa, pl, 1, 0);
+                    multiply(pb, q0f, sc, 1);
+                    read_p(pb, pl, 1, 1);
+                    multiply(pa, q1f, sc, 0);
                 }
-                p.load_part(p0, 0);
-                q.load_part(q0, 0);
-                first_step(p1, q1);
-                __syncthreads();
-            } else {
-                first_step(p0, q0);
-                wait_loads_and_sync();
-                read_scales(sa, 0);
-                fetch(p1, q1);
+                if constexpr (more()) {
+                    wait_loads_and_sync();
+                    if constexpr (fetch_more()) fetch(pl, ql);
+                    read_q(FP8 ? q1f : q0f, qn, 0);
+                    read_p(pa, pn, 0, 0);
+                }
+                multiply(pb, FP8 ? q0f : q1f, sc, 1);
+            };
+            constexpr std::true_type yes{};
+            constexpr std::false_type no{};
+            if (total_steps > 0) {
+                __syncthreads();  // the previous tile's readers are done
+                auto first_step = [&](char *pl, char *ql) {
+                    if (left > 0) {
+                        // k of grad input is bytes of dpre, rows of the weight
+                        p.load_part(pl, MODE == kGradInput ? left / 2 : left);
+                        q.load_part(ql, left);
+                    } else {
+                        fetch(pl, ql);
+                    }
+                };
+                load_scales(0);
+                if (pad) {
+                    if constexpr (FP8) {
+#pragma unroll
+                        for (int t = 0; t < TF; ++t) sa.x[t] = 0.0f;
+                        sa.w[0] = sa.w[1] = 0.0f;
+                    }
+                    p.load_part(p0, 0);
+                    q.load_part(q0, 0);
+                    first_step(p1, q1);
+                    __syncthreads();
+                } else {
+                    first_step(p0, q0);
+                    wait_loads_and_sync();
+                    read_scales(sa, 0);
+                    fetch(p1, q1);
+                }
+                read_q(qa, q0, 0);
+                read_p(pa, p0, 0, 0);
+                int s = 0;
+                for (; s + 2 < total_steps; s += 2) {
+                    step(p0, q0, p1, q1, qa, qb, sa, sb, s, yes, yes);
+                    step(p1, q1, p0, q0, FP8 ? qb : qa, FP8 ? qa : qb, sb, sa, s + 1, yes, yes);
+                }
+                step(p0, q0, p1, q1, qa, qb, sa, sb, s, no, yes);
+                step(p1, q1, p0, q0, FP8 ? qb : qa, FP8 ? qa : qb, sb, sa, s + 1, no, no);
             }
-            read_q(qa, q0, 0);
-            read_p(pa, p0, 0, 0);
-            int s = 0;
-            for (; s + 2 < total_steps; s += 2) {
-                step(p0, q0, p1, q1, qa, qb, sa, sb, s, yes, yes);
-                step(p1, q1, p0, q0, FP8 ? qb : qa, FP8 ? qa : qb, sb, sa, s + 1, yes, yes);
-            }
-            step(p0, q0, p1, q1, qa, qb, sa, sb, s, no, yes);
-            step(p1, q1, p0, q0, FP8 ? qb : qa, FP8 ? qa : qb, sb, sa, s + 1, no, no);
-        }
         };
         if (live == TF) {
             accumulate(std::integral_constant<int, TF>{});
@@ -636,6 +637,12 @@ hipError_t launch_tiled(const Args &a, hipStream_t stream) {
 
 template <int MODE, int ACT, bool FP8, class Args>
 hipError_t launch_sized(const Args &a, hipStream_t stream) {
+    if constexpr (MODE == kForward) {
+        // 64 x 64 tiles where 128 outputs a workgroup would leave CUs idle
+        // (37 x 2048 x 7168: 11.4 us against 13.9)
+        if (a.mean_rows <= 64 && a.seg.E * ((a.M + 127) / 128) < kCUs)
+            return launch_tiled<MODE, ACT, FP8, 1, 4, 4, 1>(a, stream);
+    }
     if constexpr (FP8) {
         return launch_tiled<MODE, ACT, true, 2, 2, 4, 4>(a, stream);
     } else {
@@ -668,17 +675,22 @@ int32_t grad_row_ranges(int32_t E, int32_t N) {
     return static_cast<int32_t>(s < 1 ? 1 : s > 64 ? 64 : s);
 }
 
-// Which products take the kernel for few rows: experts of up to 8 rows on
-// average, and up to 48 where the tiled product's 128 outputs a workgroup
-// would leave most CUs idle.
-bool few_rows(const ProductArgs &a) {
-    if (a.mean_rows <= 8) return true;
+// Which products take the kernel for few rows.  In bf16, experts of up to 8
+// rows on average: 64 experts of 4096 -> 2 x 1408 took 276, 282 and 288 us at
+// 4, 6 and 8 rows against the tiled product's 310, and 303 against 311 at 12
+// but 424 against 317 at 24.  Not in FP8, where the tiled product's 128-byte
+// rows of loads are ahead (310 us against 395 at 4 rows, 64 experts of 7168 ->
+// 2 x 2048; 326 against 314, 128 experts of 4096 -> 2 x 1408).  Either type up
+// to 16 rows where tiles of 128 outputs would leave CUs idle (16 x 2048 x 7168:
+// 11.2 us against 12.0; 16 x 7168 x 2048: 16 against 30).
+bool few_rows(const ProductArgs &a, bool fp8) {
+    if (!fp8 && a.mean_rows <= 8) return true;
     const int64_t tiles = a.seg.E * ((a.M + 127) / 128);
-    return a.mean_rows <= 48 && tiles < kCUs;
+    return a.mean_rows <= 16 && tiles < kCUs;
 }
 
 hipError_t launch_product(const ProductArgs &a, bool fp8, hipStream_t stream) {
-    if (few_rows(a)) return launch_product_few(a, fp8, stream);
+    if (few_rows(a, fp8)) return launch_product_few(a, fp8, stream);
     return fp8 ? launch_forward<true>(a, stream) : launch_forward<false>(a, stream);
 }
 

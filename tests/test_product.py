@@ -65,6 +65,7 @@ CASES = [
     (700, 256, 520, 4, 2, 2, 1, "geglu", True, True, True),
     (1100, 328, 392, 2, 2, 1, 1, "silu", True, True, True),
     (600, 64, 264, 1, 1, 1, 1, "swiglu", False, False, True),
+    (90, 328, 1096, 2, 1, 1, 1, "geglu", True, True, True),    # small tiles, gated
     (9, 264, 1000, 3, 1, 1, 1, "gelu", True, True, False),     # few rows, several tiles of outputs
     (150, 1032, 72, 2, 1, 2, 1, "relu", False, False, True),   # an odd number of steps and a part step
     (4000, 72, 8200, 16, 2, 4, 1, "none", False, False, False),  # more tiles than workgroups
@@ -194,6 +195,8 @@ FP8_CASES = [
     (513, 256, 128, 1, 1, 1, "silu", "column", True, True),
     (260, 1152, 128, 2, 2, 1, "none", "padded", False, False),
     (90, 1664, 256, 2, 1, 1, "geglu", "column", True, False),
+    (11, 384, 256, 3, 2, 1, "swiglu", "padded", True, True),
+    (40, 256, 128, 300, 2, 2, "silu", "token", False, True),
 ]
 
 
