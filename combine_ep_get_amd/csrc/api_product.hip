@@ -220,6 +220,7 @@ int ep_expert_product_backward(const ep_problem *p, const ep_product *q, const u
     a.dweight_acc = dweight_acc;
     a.dbias = dbias;
     a.partial = dbias ? reinterpret_cast<float *>(static_cast<char *>(workspace) + 256) : nullptr;
+    a.entries = static_cast<int64_t>(p->num_tokens) * p->num_topk;
     a.mean_rows = mean_rows(p);
     a.splits = epget::grad_row_ranges(p->num_experts, q->out_features);
     return hip_rc(epget::launch_product_grad(a, static_cast<hipStream_t>(stream)));

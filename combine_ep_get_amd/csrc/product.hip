@@ -629,9 +629,17 @@ constexpr int kCUs = 256;
 
 template <int MODE, int ACT, bool FP8, int WF, int WT, int FF, int TF, class Args>
 hipError_t launch_tiled(const Args &a, hipStream_t stream) {
-    // persistent workgroups: as many as the CUs' LDS holds (two buffers of both tiles)
+    // persistent workgroups: as many as the CUs' LDS holds (two buffers of both
+    // tiles), and no more than there can be tiles
     constexpr int kPerCU = WF * WT > 4 ? 1 : 2;
-    product_kernel<MODE, ACT, FP8, WF, WT, FF, TF><<<kCUs * kPerCU, 64 * WF * WT, 0, stream>>>(a);
+    constexpr int BF = WF * FF * 16, BT = WT * TF * 16;
+    const int64_t features = MODE == kForward ? a.M : a.C;
+    const int64_t nf = (features + BF - 1) / BF;
+    const int64_t row_tiles = MODE == kGradWeight ? static_cast<int64_t>(a.seg.E) * ((a.M + BT - 1) / BT)
+                                                  : a.entries / BT + min(static_cast<int64_t>(a.seg.E), a.entries);
+    const int64_t tiles = row_tiles * nf;
+    const uint32_t grid = static_cast<uint32_t>(max(int64_t{8}, min(int64_t{kCUs * kPerCU}, (tiles + 7) / 8 * 8)));
+    product_kernel<MODE, ACT, FP8, WF, WT, FF, TF><<<grid, 64 * WF * WT, 0, stream>>>(a);
     return hipGetLastError();
 }
 

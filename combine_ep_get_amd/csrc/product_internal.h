@@ -39,6 +39,7 @@ struct ProductGradArgs {
     uint16_t *dpre;  // gradient of the pre-activations: dout itself without an activation
     uint16_t *dx, *dweight;
     float *dweight_acc, *dbias, *partial;
+    int64_t entries;
     int32_t splits;  // row ranges of an expert whose bias gradients are summed apart
     int64_t mean_rows;
 };
