@@ -626,6 +626,14 @@ __global__ __launch_bounds__(256) void bias_join_kernel(const float *__restrict_
 }
 
 constexpr int kCUs = 256;
+constexpr int kLargeTiles = 192;
+
+// Tiles of a product in the worst case, each expert's last one in part filled.
+template <int MODE, class Args>
+int64_t most_tiles(const Args &a, int64_t BF, int64_t BT) {
+    const int64_t nf = ((MODE == kForward ? a.M : a.C) + BF - 1) / BF, E = a.seg.E;
+    return nf * (MODE == kGradWeight ? E * ((a.M + BT - 1) / BT) : a.entries / BT + min(E, a.entries));
+}
 
 template <int MODE, int ACT, bool FP8, int WF, int WT, int FF, int TF, class Args>
 hipError_t launch_tiled(const Args &a, hipStream_t stream) {
@@ -633,11 +641,7 @@ hipError_t launch_tiled(const Args &a, hipStream_t stream) {
     // tiles), and no more than there can be tiles
     constexpr int kPerCU = WF * WT > 4 ? 1 : 2;
     constexpr int BF = WF * FF * 16, BT = WT * TF * 16;
-    const int64_t features = MODE == kForward ? a.M : a.C;
-    const int64_t nf = (features + BF - 1) / BF;
-    const int64_t row_tiles = MODE == kGradWeight ? static_cast<int64_t>(a.seg.E) * ((a.M + BT - 1) / BT)
-                                                  : a.entries / BT + min(static_cast<int64_t>(a.seg.E), a.entries);
-    const int64_t tiles = row_tiles * nf;
+    const int64_t tiles = most_tiles<MODE>(a, BF, BT);
     const uint32_t grid = static_cast<uint32_t>(max(int64_t{8}, min(int64_t{kCUs * kPerCU}, (tiles + 7) / 8 * 8)));
     product_kernel<MODE, ACT, FP8, WF, WT, FF, TF><<<grid, 64 * WF * WT, 0, stream>>>(a);
     return hipGetLastError();
@@ -654,7 +658,9 @@ hipError_t launch_sized(const Args &a, hipStream_t stream) {
     if constexpr (FP8) {
         return launch_tiled<MODE, ACT, true, 2, 2, 4, 4>(a, stream);
     } else {
-        if (a.mean_rows >= (MODE == kForward ? 160 : 64)) return launch_tiled<MODE, ACT, false, 2, 4, 8, 4>(a, stream);
+        // large tiles where the rows fill them and every CU has one
+        if (a.mean_rows >= (MODE == kForward ? 160 : 64) && most_tiles<MODE>(a, 256, 256) >= kLargeTiles)
+            return launch_tiled<MODE, ACT, false, 2, 4, 8, 4>(a, stream);
         return launch_tiled<MODE, ACT, false, 2, 2, 4, 4>(a, stream);
     }
 }
