@@ -626,7 +626,11 @@ __global__ __launch_bounds__(256) void bias_join_kernel(const float *__restrict_
 }
 
 constexpr int kCUs = 256;
-constexpr int kLargeTiles = 192;
+// Tiles from which the larger sizes are taken: 200 x 2048 x 2048 takes 12 us
+// in 64 x 64 tiles and 20 in 32 of 128 x 128, but the weight gradient of
+// 16384 x 512 x 4096 185 us and 148 (128 tiles); 2048 x 2048 x 2048 26 us in
+// 256 tiles of 128 x 128 and 46 in 64 of 256 x 256.
+constexpr int kMediumTiles = 128, kLargeTiles = 192;
 
 // Tiles of a product in the worst case, each expert's last one in part filled.
 template <int MODE, class Args>
@@ -649,12 +653,8 @@ hipError_t launch_tiled(const Args &a, hipStream_t stream) {
 
 template <int MODE, int ACT, bool FP8, class Args>
 hipError_t launch_sized(const Args &a, hipStream_t stream) {
-    if constexpr (MODE == kForward) {
-        // 64 x 64 tiles where 128 outputs a workgroup would leave CUs idle
-        // (37 x 2048 x 7168: 11.4 us against 13.9)
-        if (a.mean_rows <= 64 && a.seg.E * ((a.M + 127) / 128) < kCUs)
-            return launch_tiled<MODE, ACT, FP8, 1, 4, 4, 1>(a, stream);
-    }
+    // 64 x 64 tiles where larger ones would leave most CUs idle
+    if (most_tiles<MODE>(a, 128, 128) < kMediumTiles) return launch_tiled<MODE, ACT, FP8, 1, 4, 4, 1>(a, stream);
     if constexpr (FP8) {
         return launch_tiled<MODE, ACT, true, 2, 2, 4, 4>(a, stream);
     } else {

@@ -68,6 +68,8 @@ CASES = [
     (90, 328, 1096, 2, 1, 1, 1, "geglu", True, True, True),    # small tiles, gated
     (9, 264, 1000, 3, 1, 1, 1, "gelu", True, True, False),     # few rows, several tiles of outputs
     (150, 1032, 72, 2, 1, 2, 1, "relu", False, False, True),   # an odd number of steps and a part step
+    (700, 264, 4360, 8, 1, 2, 1, "silu", True, True, True),      # 128 x 128 tiles
+    (300, 136, 2056, 4, 1, 1, 1, "swiglu", True, False, True),   # the same, gated
     (4000, 72, 8200, 16, 2, 4, 1, "none", False, False, False),  # more tiles than workgroups
 ]
 
@@ -195,6 +197,7 @@ FP8_CASES = [
     (513, 256, 128, 1, 1, 1, "silu", "column", True, True),
     (260, 1152, 128, 2, 2, 1, "none", "padded", False, False),
     (90, 1664, 256, 2, 1, 1, "geglu", "column", True, False),
+    (400, 640, 2048, 8, 1, 1, "swiglu", "padded", True, True),   # 128 x 128 tiles
     (11, 384, 256, 3, 2, 1, "swiglu", "padded", True, True),
     (40, 256, 128, 300, 2, 2, "silu", "token", False, True),
 ]

@@ -16,6 +16,8 @@ CASES = [
     (257, 136, 72, 5, 3, 5, 1, "relu"),
     (300, 264, 200, 4, 2, 2, 1, "none"),
     (1300, 264, 328, 2, 2, 1, 1, "swiglu"),
+    (300, 2056, 136, 8, 1, 1, 1, "geglu"),    # 128 x 128 tiles
+    (2400, 2056, 136, 24, 1, 2, 1, "silu"),   # 256 x 256 tiles
 ]
 
 
