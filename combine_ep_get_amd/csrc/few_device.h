@@ -5,6 +5,8 @@
 // few-token layer and the expert products of few rows.
 #pragma once
 
+#include <type_traits>
+
 #include "product_device.h"
 
 namespace epget {

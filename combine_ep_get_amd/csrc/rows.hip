@@ -238,7 +238,7 @@ __global__ __launch_bounds__(kNarrowThreads) void combine_narrow_kernel(
 // vector of dy, so dy may be y.
 //
 // Bound by HBM: 4.0 GB for 16384 tokens of 8 entries and 7168 channels.  With
-// one entry a workgroup dout is read again for each (1113 us against 880),
+// one entry a workgroup dout is read again for each (1113 us against 770-805),
 // but a batch of under kGradTokens tokens needs the workgroups (128 tokens: 6.8 us).
 constexpr int kGradMaxThreads = 512;
 constexpr int kGradTokens = 1024;

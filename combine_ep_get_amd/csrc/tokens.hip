@@ -11,11 +11,13 @@
 // order.  Scaling h by its weight lets the down product sum a token's
 // experts with no further factors.
 //
+// Measured: one token of top-8 of 64 experts (7168 -> 2 x 2048 -> 7168, 705 MB) 147-156
+// us, 128 tokens of top-8 of 256 (22 GB) 4.4 ms: 4.5-5.1 TB/s, where a large
+// copy reaches 4.7 and a streaming read 5.2.
+//
 // Every workgroup first sorts the entries by expert in LDS: at most
 // kMaxTokens * EP_MAX_TOPK ids, which stay in L2.  A token that names an
 // expert twice keeps one entry, with the sum of both weights.
-#include <type_traits>
-
 #include "few_device.h"
 
 namespace epget {
