@@ -242,6 +242,9 @@ __global__ __launch_bounds__(kNarrowThreads) void combine_narrow_kernel(
 // but a batch of under kGradTokens tokens needs the workgroups (128 tokens: 6.8 us).
 constexpr int kGradMaxThreads = 512;
 constexpr int kGradTokens = 1024;
+// Tokens of one launch: HIP counts a launch's threads in 32 bits, and a grid
+// of more is not refused but wraps.
+constexpr int64_t kGradLaunchTokens = ((int64_t{1} << 32) - 1) / kGradMaxThreads;
 
 template <int KG>
 __global__ __launch_bounds__(kGradMaxThreads) void combine_backward_kernel(
@@ -434,14 +437,22 @@ hipError_t launch_combine_backward(const CopyParams &c, const uint16_t *dout, co
     const bool few = c.T < kGradTokens;
     // two vectors a thread, or one for rows of less than that
     const int want = (c.nvec + 1) / 2, threads = min(kGradMaxThreads, (want + 63) / 64 * 64);
-    const dim3 grid(c.T, few ? c.K : 1);
-    if (few || c.K == 1)
-        combine_backward_kernel<1><<<grid, threads, 0, stream>>>(dout, y, slot, w, dy, dw, c.H, c.K, c.nvec, c.num_rows);
-    else if (c.K <= 4)
-        combine_backward_kernel<4><<<grid, threads, 0, stream>>>(dout, y, slot, w, dy, dw, c.H, c.K, c.nvec, c.num_rows);
-    else
-        combine_backward_kernel<8><<<grid, threads, 0, stream>>>(dout, y, slot, w, dy, dw, c.H, c.K, c.nvec, c.num_rows);
-    return hipGetLastError();
+    for (int64_t t = 0; t < c.T; t += kGradLaunchTokens) {
+        const dim3 grid(static_cast<uint32_t>(min(kGradLaunchTokens, c.T - t)), few ? c.K : 1);
+        const uint16_t *d = dout + t * c.H;
+        const int32_t *sl = slot + t * c.K;
+        const float *wt = w ? w + t * c.K : nullptr;
+        float *to = dw ? dw + t * c.K : nullptr;
+        if (few || c.K == 1)
+            combine_backward_kernel<1><<<grid, threads, 0, stream>>>(d, y, sl, wt, dy, to, c.H, c.K, c.nvec, c.num_rows);
+        else if (c.K <= 4)
+            combine_backward_kernel<4><<<grid, threads, 0, stream>>>(d, y, sl, wt, dy, to, c.H, c.K, c.nvec, c.num_rows);
+        else
+            combine_backward_kernel<8><<<grid, threads, 0, stream>>>(d, y, sl, wt, dy, to, c.H, c.K, c.nvec, c.num_rows);
+        const hipError_t rc = hipGetLastError();
+        if (rc != hipSuccess) return rc;
+    }
+    return hipSuccess;
 }
 
 hipError_t launch_combine_weights(const CopyParams &c, const float *recv_w, const int32_t *slot,
