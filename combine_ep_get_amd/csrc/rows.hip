@@ -235,7 +235,8 @@ __global__ __launch_bounds__(kNarrowThreads) void combine_narrow_kernel(
 // flight and dout read once for all of them; the sums are joined over the
 // lanes by halves, then over the waves in order.  y and dy pass once and carry
 // the non-temporal hint.  A thread reads its vector of y before it writes the same
-// vector of dy, so dy may be y.
+// vector of dy, and an entry without a slot (or past the last one of a group) reads
+// no row, so dy may be y.
 //
 // Bound by HBM: 4.0 GB for 16384 tokens of 8 entries and 7168 channels.  With
 // one entry a workgroup dout is read again for each (1113 us against 770-805),
@@ -263,7 +264,7 @@ __global__ __launch_bounds__(kGradMaxThreads) void combine_backward_kernel(
             const int64_t i = t * K + min(j0 + j, K - 1);
             const int32_t s = slot[i];
             ok[j] = j0 + j < K && slot_ok(s, num_rows);
-            row[j] = ok[j] ? s : 0;  // row 0 is in bounds; what comes of it is dropped
+            row[j] = s;
             wj[j] = w ? w[i] : 1.0f;
             sum[j] = 0.0f;
         }
@@ -273,7 +274,8 @@ __global__ __launch_bounds__(kGradMaxThreads) void combine_backward_kernel(
             if (dw) {
 #pragma unroll
                 for (int j = 0; j < KG; ++j)
-                    in[j] = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(y + row[j] * H) + v);
+                    in[j] = ok[j] ? __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(y + row[j] * H) + v)
+                                  : u32x4{0, 0, 0, 0};
             }
 #pragma unroll
             for (int j = 0; j < KG; ++j) {

@@ -3,7 +3,8 @@ the kernel that takes large batches."""
 import pytest
 import torch
 
-from test_product import ep  # noqa: F401
+import product_reference as ref
+from test_product import Routed, ep, marked, normal, untouched  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -30,3 +31,56 @@ def test_more_tokens_than_one_launch_holds(ep):  # noqa: F811
         want_dy[i + 1] = (i - 3) * (i + 2)
     assert torch.equal(dw, want)
     assert torch.equal(dy.float().cpu(), want_dy)
+
+
+@pytest.mark.parametrize("T,H,E,K,R,empty", [
+    (1100, 264, 32, 8, 4, 0.1),    # eight entries at a time
+    (1030, 136, 24, 5, 2, 0.3),    # a group that is not full
+    (1100, 136, 40, 20, 4, 0.1),   # three groups, the last of four
+    (1024, 1032, 16, 12, 1, 0.0),  # the smallest batch of this kernel, more than one wave
+    (1500, 72, 8, 3, 2, 0.5),      # four at a time
+])
+def test_large_batches(ep, T, H, E, K, R, empty):  # noqa: F811
+    r = Routed(ep, T, E, K, R, hidden=H, empty=empty, seed=T + K)
+    g = torch.Generator().manual_seed(K)
+    dout, y, w = normal(g, T, H), normal(g, r.rows, H), torch.randn(T, K, generator=g)
+    # rows that no slot names are not read: row 0 may be one of them
+    unused = torch.ones(r.rows, dtype=torch.bool)
+    unused[r.used] = False
+    y[unused] = float("nan")
+    dy, dw = marked(r.rows, H), torch.full((T, K), 7.0, device="cuda")
+    cd, cy, cw = dout.cuda(), y.cuda(), w.cuda()
+    ep.ep_combine_backward(r.p, cd, cy, r.bufs.token_slot, cw, dy, dw)
+    ok, vy, by, vw, bw = ref.combine_backward(dout, y.nan_to_num(0.0), r.slot, w, r.rows)
+    at = r.slot[ok].long().cuda()
+    ref.assert_within(dy[at], vy[ok], by[ok], "dy")
+    ref.assert_within(dw, vw, bw, "dweights")
+    assert untouched(dy, at)
+    # each alone, and dy in y's place: the same bits
+    dy2, dw2 = marked(r.rows, H), torch.empty_like(dw)
+    ep.ep_combine_backward(r.p, cd, None, r.bufs.token_slot, cw, dy2, None)
+    assert torch.equal(dy2.view(torch.int16), dy.view(torch.int16))
+    ep.ep_combine_backward(r.p, cd, cy, r.bufs.token_slot, cw, None, dw2)
+    assert torch.equal(dw2, dw)
+    for _ in range(3):
+        cy, dw2 = y.cuda(), torch.empty_like(dw)
+        ep.ep_combine_backward(r.p, cd, cy, r.bufs.token_slot, cw, cy, dw2)
+        assert torch.equal(cy.view(torch.int16)[at], dy.view(torch.int16)[at]) and torch.equal(dw2, dw)
+        assert torch.isnan(cy[unused.cuda()]).all()
+
+
+@pytest.mark.parametrize("T", [40, 1100])
+def test_first_row_belongs_to_another_token(ep, T):  # noqa: F811
+    """Row 0 is named by the last token, in whose place its gradient is
+    written, while every other token has empty entries."""
+    H, K = 136, 6
+    g = torch.Generator().manual_seed(T)
+    slot = torch.full((T, K), -1, dtype=torch.int32)
+    slot[:, 2] = torch.arange(T, 0, -1) - 1
+    p = ep.Problem.make(T, H, 8, K, 1, 1, 1, T)
+    dout, y = normal(g, T, H), normal(g, T, H)
+    cy, dw = y.cuda(), torch.full((T, K), 7.0, device="cuda")
+    ep.ep_combine_backward(p, dout.cuda(), cy, slot.cuda(), None, cy, dw)
+    ok, vy, by, vw, bw = ref.combine_backward(dout, y, slot, None, T)
+    assert torch.equal(cy.cpu(), dout.flip(0))
+    ref.assert_within(dw, vw, bw, "dweights")
