@@ -67,12 +67,12 @@ struct ColumnBlock {
     u32x4 v[kPieces];
 
     template <bool FULL>
-    __device__ __forceinline__ void load(const char *col, int b, int K, int lg, bool live = true) {
+    __device__ __forceinline__ void load(const char *col, int b, int K, int lg) {
 #pragma unroll
         for (int s = 0; s < kPieces; ++s) {
             const int k = b * kBlockK + (XFP8 ? 64 * s + 16 * lg : WFP8 ? 64 * (s >> 1) + 16 * lg + 8 * (s & 1) : 32 * s + 8 * lg);
             const u32x4 *p = reinterpret_cast<const u32x4 *>(col + static_cast<int64_t>(k) * (XFP8 ? 1 : 2));
-            v[s] = live && (FULL || k < K) ? *p : u32x4{0, 0, 0, 0};
+            v[s] = FULL || k < K ? *p : u32x4{0, 0, 0, 0};
         }
     }
 };

@@ -58,8 +58,6 @@ struct TokensArgs {
     uint16_t *h;  // [T * K, I] hidden rows, scaled by their weights
 };
 
-constexpr int kMaxTokens = 128;  // EP_MOE_TOKENS_MAX
-
 // Row ranges that each expert's rows are cut into for the elementwise pass of
 // the backward call; the bias gradients are summed by range, then joined.
 int32_t grad_row_ranges(int32_t E, int32_t N);

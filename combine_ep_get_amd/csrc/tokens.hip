@@ -16,14 +16,15 @@
 // copy reaches 4.7 and a streaming read 5.2.
 //
 // Every workgroup first sorts the entries by expert in LDS: at most
-// kMaxTokens * EP_MAX_TOPK ids, which stay in L2.  A token that names an
+// EP_MOE_TOKENS_MAX * EP_MAX_TOPK ids, which stay in L2.  A token that names an
 // expert twice keeps one entry, with the sum of both weights.
 #include "few_device.h"
 
 namespace epget {
 namespace {
 
-constexpr int kMaxEntries = kMaxTokens * EP_MAX_TOPK;
+constexpr int kMaxEntries = EP_MOE_TOKENS_MAX * EP_MAX_TOPK;
+static_assert(kMaxEntries <= 65536 && EP_MAX_EXPERTS <= 32768, "entries are 16-bit numbers, ids signed ones");
 
 struct EntryLists {
     int end[EP_MAX_EXPERTS];             // end of expert e's run in `entry` (its start is end[e - 1])
@@ -293,6 +294,7 @@ hipError_t launch_down(const TokensArgs &a, hipStream_t stream) {
     // workgroup anyway and there are enough of them, else 16
     const int ff = a.T > 64 && a.H >= 4096 ? 2 : 1;
     const uint32_t grid = (a.H + 16 * ff - 1) / (16 * ff), lds = kFewWaves * a.T * 16 * ff * 4;
+    static_assert(sizeof(EntryLists) + kFewWaves * EP_MOE_TOKENS_MAX * 16 * 2 * 4 <= 160 * 1024, "a CU's LDS");
     if (ff == 2)
         tokens_down_kernel<FP8, 2, true><<<grid, kFewThreads, lds, stream>>>(a);
     else if (a.T > 16)
