@@ -440,7 +440,11 @@ int ep_expert_product(const ep_problem *problem, const ep_product *product, cons
  *   x_sf  fp32 device, strides >= 1 as for ep_dispatch_fp8
  *   w_fp8 [E,M,C] uint8 device, 16-byte aligned
  *   w_sf  [E,M/128,C/128] fp32 device
- *   the others as for ep_expert_product */
+ *   the others as for ep_expert_product
+ * out is bf16: for a second FP8 product, ep_quantize_fp8 turns it into codes
+ * and scales, with a problem of num_tokens = R*S, hidden = N and
+ * num_experts = num_topk = num_ranks = 1 (rows of no expert are converted as
+ * well, whatever they hold, and not read by the product). */
 int ep_expert_product_fp8(const ep_problem *problem, const ep_product *product,
                           const uint8_t *x_fp8, const float *x_sf, int64_t sf_token_stride,
                           int64_t sf_hidden_stride, const int32_t *expert_count,
