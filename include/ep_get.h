@@ -410,8 +410,9 @@ int ep_combine_backward(const ep_problem *problem, const uint16_t *dout, const u
  * with fp32 sums and one rounding.  The rows of expert e are
  * expert_count[e] rows from row rank(e)*S + expert_offset[e] on, cut off at
  * the end of its slice, as ep_get_layout leaves them; other rows of x are not
- * read and of out and pre not written.  problem->hidden and the batch's
- * size only guide the choice of a kernel.
+ * read and of out and pre not written.  A batch of no tokens has no rows,
+ * whatever the arrays hold; else problem->hidden and the batch's size only
+ * guide the choice of a kernel.
  * A dense product is num_experts = num_topk = num_ranks = 1 and NULL for
  * both arrays: rows [0, T).
  *
@@ -478,7 +479,8 @@ size_t ep_product_workspace_bytes(const ep_problem *problem, const ep_product *p
  *   workspace   ep_product_workspace_bytes bytes, 256-byte aligned; calls
  *               that may overlap need one each; NULL (with 0 bytes) without
  *               dbias
- * bf16 and fp32 arrays are 16-byte aligned. */
+ * bf16 and fp32 arrays are 16-byte aligned, and but for pre and dpre no
+ * output overlaps another array. */
 int ep_expert_product_backward(const ep_problem *problem, const ep_product *product,
                                const uint16_t *dout, const uint16_t *pre, const uint16_t *x,
                                const int32_t *expert_count, const int32_t *expert_offset,
