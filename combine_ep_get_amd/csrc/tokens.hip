@@ -291,8 +291,12 @@ hipError_t launch_up(const TokensArgs &a, hipStream_t stream) {
 template <bool FP8>
 hipError_t launch_down(const TokensArgs &a, hipStream_t stream) {
     // 32 outputs a workgroup where the tokens' sums leave a CU's LDS to one
-    // workgroup anyway and there are enough of them, else 16
-    const int ff = a.T > 64 && a.H >= 4096 ? 2 : 1;
+    // workgroup or two anyway and 16 would take more than one workgroup a CU,
+    // else 16.  The layer for 128 tokens with 16 and with 32: 256 experts of
+    // 7168 x 2048 4602 and 4412 us, 128 of 4608 x 2048 1920 and 1767, but 256
+    // of 4096 x 2048 2491 and 2981; in FP8 2708 and 2442, 1142 and 1026, 1389
+    // and 1668.
+    const int ff = a.T > 64 && a.H > 16 * kTokenCUs ? 2 : 1;
     const uint32_t grid = (a.H + 16 * ff - 1) / (16 * ff), lds = kFewWaves * a.T * 16 * ff * 4;
     static_assert(sizeof(EntryLists) + kFewWaves * EP_MOE_TOKENS_MAX * 16 * 2 * 4 <= 160 * 1024, "a CU's LDS");
     if (ff == 2)

@@ -1,7 +1,7 @@
 """The few-token layer on the kernels that its large calls take: waves of the up
 product that work alone (from 1024 pairs of an expert and 16 outputs), 16 and 32
 columns at a time, and 32 outputs a workgroup of the down product (more than
-64 tokens and 4096 channels or more)."""
+64 tokens and 4096 channels)."""
 import pytest
 import torch
 
@@ -45,10 +45,12 @@ CASES = [
     (100, 264, 264, 64, 8, "geglu", False, False),
     (128, 200, 264, 64, 6, "silu", True, False),
     (128, 136, 272, 64, 4, "none", False, True),
-    # 32 outputs a workgroup, the last one half full (4104) or whole
+    # 32 outputs a workgroup, the last one a quarter full (4104) or whole
     (65, 4104, 40, 8, 4, "swiglu", True, True),
     (128, 4104, 136, 8, 3, "gelu", True, False),
-    (128, 4096, 72, 4, 2, "relu", False, True),
+    (128, 4128, 72, 4, 2, "relu", False, True),
+    # the widest with 16
+    (128, 4096, 72, 4, 2, "silu", True, True),
     # both
     (128, 4104, 272, 64, 8, "swiglu", True, True),
 ]
@@ -91,6 +93,7 @@ FP8_CASES = [
     (100, 128, 384, 64, 6, "silu", False),
     (128, 4096, 128, 4, 2, "geglu", True),
     (65, 4224, 128, 8, 4, "none", True),
+    (128, 4352, 128, 4, 2, "geglu", True),
     (128, 4224, 256, 64, 4, "swiglu", False),
 ]
 
