@@ -4,11 +4,10 @@
 //
 // One workgroup takes up to 16 rows of an expert and 16 outputs (32 weight
 // rows when gated), its waves the blocks of k in turn; the sums are joined in
-// LDS in a fixed order.  A tile of the tiled product would spend its LDS traffic and
-// barriers on rows that are not there, and its grid of 128 outputs a
-// workgroup leaves most of the chip idle on one small product.  With
-// kWaveItems tiles or more each wave takes tiles of its own, over all of k: 64
-// experts of 4 rows, 4096 -> 2 x 1408 (1.5 GB of weights), in 276-284 us, 5.2 TB/s.
+// LDS in a fixed order.  The tiled product's grid of 64 or 128 outputs a
+// workgroup leaves most of the chip idle on one small product, and its waves
+// wait at each step for one another: 16 x 4096 x 8192 takes 19.7 us here (3.4
+// TB/s), 31.0 there.
 #include "few_device.h"
 
 namespace epget {
@@ -33,10 +32,9 @@ __global__ __launch_bounds__(kFewThreads) void product_few_kernel(ProductArgs a)
     const int nf = (a.N + 15) / 16;
     const int64_t total = static_cast<int64_t>(first[a.seg.E]) * nf;
     const int64_t pitch = static_cast<int64_t>(a.C) * (FP8 ? 1 : 2);
-    const bool alone = total >= kWaveItems;
-    const int G = gridDim.x * (alone ? kFewWaves : 1), worker = blockIdx.x + (alone ? wave * gridDim.x : 0);
+    const int G = gridDim.x;
     for (int64_t round = 0; round * G < total; ++round) {
-        const int64_t tile = tile_of(total, round, worker, G);
+        const int64_t tile = tile_of(total, round, blockIdx.x, G);
         if (tile < 0) break;
         const int e = tile_expert(first, a.seg.E, static_cast<int>(tile / nf));
         const int f0 = __builtin_amdgcn_readfirstlane(first[e]);
@@ -61,19 +59,12 @@ __global__ __launch_bounds__(kFewThreads) void product_few_kernel(ProductArgs a)
         const float *const x_sf[1] = {FP8 ? a.x_sf + xr * a.sf_ts : nullptr};
         // neighbouring tiles start at different blocks of k, so that they do
         // not all read the same piece of x at once (1.5 us of 14)
-        accumulate_blocks<FP8, FP8>(acc, row, col, w_sf, x_sf, a.sf_hs, a.C, alone ? 0 : (wave + ft) % kFewWaves,
-                                    alone ? 1 : kFewWaves, lg);
+        accumulate_blocks<FP8, FP8>(acc, row, col, w_sf, x_sf, a.sf_hs, a.C, (wave + ft) % kFewWaves, kFewWaves, lg);
         const int tok = t0 + li, n = n0 + lg * 4;
-        const bool mine = tok < rows && n < a.N;
-        if (alone) {
-            f32x4 v[1] = {acc[0][0]}, u[1] = {acc[FF - 1][0]};
-            if (mine) write_outputs<ACT>(a, e, row0 + tok, n, v, u);
-            continue;
-        }
 #pragma unroll
         for (int f = 0; f < FF; ++f) part[wave][f][lane] = acc[f][0];
         __syncthreads();
-        if (wave == 0 && mine) {
+        if (wave == 0 && tok < rows && n < a.N) {
             f32x4 v[1] = {sum_waves(&part[0][0][lane], FF * 64)};
             f32x4 u[1] = {GATED ? sum_waves(&part[0][FF - 1][lane], FF * 64) : v[0]};
             write_outputs<ACT>(a, e, row0 + tok, n, v, u);

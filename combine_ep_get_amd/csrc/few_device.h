@@ -15,11 +15,6 @@ namespace {
 constexpr int kFewThreads = 512;
 constexpr int kFewWaves = kFewThreads / 64;
 constexpr int kBlockK = 128;  // k per block: one scale of an FP8 weight
-// Items (16 outputs of an expert's rows) from which waves work alone, each on
-// items of its own: four waves on each of 256 CUs keep enough loads in flight,
-// and none waits for another (one token of 8 experts: 166 us with items shared by
-// a workgroup, 147 alone).
-constexpr int kWaveItems = 1024;
 
 // A block of one fragment of 16 weight rows, as it comes from memory: bf16 in
 // four pieces of 8 k a lane (k = 32 q + 8 g), e4m3 in two of 16 (k = 64 q + 16 g).

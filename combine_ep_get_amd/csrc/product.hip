@@ -689,22 +689,22 @@ int32_t grad_row_ranges(int32_t E, int32_t N) {
     return static_cast<int32_t>(s < 1 ? 1 : s > 64 ? 64 : s);
 }
 
-// Which products take the kernel for few rows.  In bf16, experts of up to 8
-// rows on average: 64 experts of 4096 -> 2 x 1408 took 276, 282 and 288 us at
-// 4, 6 and 8 rows against the tiled product's 310, and 303 against 311 at 12
-// but 424 against 317 at 24.  Not in FP8, where the tiled product's 128-byte
-// rows of loads are ahead (310 us against 395 at 4 rows, 64 experts of 7168 ->
-// 2 x 2048; 326 against 314, 128 experts of 4096 -> 2 x 1408).  Either type up
-// to 16 rows where tiles of 128 outputs would leave CUs idle (16 x 2048 x 7168:
-// 11.2 us against 12.0; 16 x 7168 x 2048: 16 against 30).
-bool few_rows(const ProductArgs &a, bool fp8) {
-    if (!fp8 && a.mean_rows <= 8) return true;
-    const int64_t tiles = a.seg.E * ((a.M + 127) / 128);
-    return a.mean_rows <= 16 && tiles < kCUs;
+// Which products take the kernel for few rows: up to 16 rows an expert on
+// average and kFewTiles tiles of 128 weight rows in all, for which the tiled
+// product starts too few workgroups (16 x 7168 x 2048, 16 tiles: 16.0 us
+// against 28.2, in FP8 11.6 against 22.1; 16 x 4096 x 8192, 64 tiles: 19.7
+// against 31.0, FP8 13.5 against 18.9).  From 65 to 96 tiles neither is ahead (+-40 %
+// by the length of k); past that the tiled product is (16 x 4096 x 16256, 127
+// tiles: 33.0 against 38.1), and more so where some experts have many rows, as
+// every 16 of them read the weight again (128 experts of 7736 -> 3560, 8 rows on
+// average by Zipf's law: 1128 us against 2211).
+constexpr int kFewTiles = 64;
+bool few_rows(const ProductArgs &a) {
+    return a.mean_rows <= 16 && int64_t{a.seg.E} * ((a.M + 127) / 128) <= kFewTiles;
 }
 
 hipError_t launch_product(const ProductArgs &a, bool fp8, hipStream_t stream) {
-    if (few_rows(a, fp8)) return launch_product_few(a, fp8, stream);
+    if (few_rows(a)) return launch_product_few(a, fp8, stream);
     return fp8 ? launch_forward<true>(a, stream) : launch_forward<false>(a, stream);
 }
 

@@ -91,6 +91,9 @@ __device__ __forceinline__ void sort_entries(const TokensArgs &a, EntryLists &l)
 // every wave of the chip, a wave takes an item by itself and waits for no
 // other; else a workgroup does, each wave a share of k, joined in LDS.
 constexpr int kTokenCUs = 256;
+// Items from which waves work alone: four waves on each of 256 CUs keep enough loads in flight
+// (one token of 8 experts: 166 us with items shared by a workgroup, 147 alone).
+constexpr int kWaveItems = 1024;
 
 // This lane's sums of columns c0 .. c0 + 16 CF - 1 of expert e's entries and
 // outputs n0 .. n0 + 15 (of both halves when gated) over a share of k.

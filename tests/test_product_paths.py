@@ -2,9 +2,8 @@
 
 The tile follows from the sizes: 64 x 64 below 128 tiles of 128 x 128; bf16
 256 x 256 from 160 rows an expert (gradients 64) and 192 such tiles; else 128 x
-128.  The kernel for few rows takes bf16 experts of up to 8 rows on average, either type
-up to 16 where fewer than 256 tiles of 128 outputs are; from 1024 tiles of 16 its
-waves work alone.  Experts' rows are uneven, so that a tile computes from one to
+128.  The kernel for few rows takes experts of up to 16 rows on average and 64 tiles of
+128 weight rows in all.  Experts' rows are uneven, so that a tile computes from one to
 all of its fragments."""
 import pytest
 import torch
@@ -47,11 +46,14 @@ FORWARD = [
     # 128 x 128
     (UNEVEN, 2, 1, 392, 1032, "swiglu", True, True, True),
     (UNEVEN, 1, 1, 328, 1096, "gelu", True, True, True),
-    # few rows, each wave by itself
+    # few rows
+    (FEW, 2, 1, 264, 248, "swiglu", True, True, True),
+    (FEW, 1, 4, 200, 256, "geglu", False, False, True),
+    (FEW, 4, 1, 1032, 504, "silu", True, True, False),
+    (FEW, 1, 1, 128, 504, "none", False, True, True),
+    # as few, but more tiles than that
     (FEW, 2, 1, 264, 1096, "swiglu", True, True, True),
-    (FEW, 1, 4, 200, 1096, "geglu", False, False, True),
     (FEW, 4, 1, 1032, 1096, "silu", True, True, False),
-    (FEW, 1, 1, 128, 1096, "none", False, True, True),
 ]
 
 
@@ -84,8 +86,9 @@ FP8 = [
     # counts, R, C, N, act, bias, residual
     (UNEVEN, 2, 1152, 1024, "swiglu", True, True),     # 128 x 128, nine blocks of scales
     (UNEVEN, 1, 1280, 2048, "silu", False, True),      # ten
-    ((58, 1, 1, 1), 1, 384, 4096, "none", True, True),  # few rows, each wave by itself
-    ((103, 1, 1, 1, 1, 1, 1), 1, 256, 2048, "geglu", True, False),
+    ((58, 1, 1, 1), 1, 384, 2048, "none", True, True),  # few rows
+    ((103, 1, 1, 1, 1, 1, 1), 1, 256, 512, "geglu", True, False),
+    ((103, 1, 1, 1, 1, 1, 1), 1, 1152, 2048, "swiglu", True, True),  # as few, but more tiles
 ]
 
 
