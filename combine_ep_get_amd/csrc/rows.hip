@@ -238,11 +238,13 @@ __global__ __launch_bounds__(kNarrowThreads) void combine_narrow_kernel(
 // vector of dy, and an entry without a slot (or past the last one of a group) reads
 // no row, so dy may be y.
 //
-// Bound by HBM: 4.0 GB for 16384 tokens of 8 entries and 7168 channels.  With
-// one entry a workgroup dout is read again for each (1113 us against 770-805),
-// but a batch of under kGradTokens tokens needs the workgroups (128 tokens: 6.8 us).
+// Bound by HBM: 4.0 GB for 16384 tokens of 8 entries and 7168 channels in 750
+// us.  With one entry a workgroup dout is read again for each (773 us), but
+// a batch of fewer than kGradTokens tokens needs the workgroups (128 tokens: 7.3 us
+// against 10.2, 1024: 47.6 against 49.1, 2048 of 2048 channels: 28.5 against 31.9;
+// 4096 tokens: 197 and 196).
 constexpr int kGradMaxThreads = 512;
-constexpr int kGradTokens = 1024;
+constexpr int kGradTokens = 4096;
 // Tokens of one launch: HIP counts a launch's threads in 32 bits, and a grid
 // of more is not refused but wraps.
 constexpr int64_t kGradLaunchTokens = ((int64_t{1} << 32) - 1) / kGradMaxThreads;

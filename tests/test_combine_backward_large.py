@@ -34,11 +34,12 @@ def test_more_tokens_than_one_launch_holds(ep):  # noqa: F811
 
 
 @pytest.mark.parametrize("T,H,E,K,R,empty", [
-    (1100, 264, 32, 8, 4, 0.1),    # eight entries at a time
-    (1030, 136, 24, 5, 2, 0.3),    # a group that is not full
-    (1100, 136, 40, 20, 4, 0.1),   # three groups, the last of four
-    (1024, 1032, 16, 12, 1, 0.0),  # the smallest batch of this kernel, more than one wave
-    (1500, 72, 8, 3, 2, 0.5),      # four at a time
+    (4200, 264, 32, 8, 4, 0.1),    # eight entries at a time
+    (4300, 136, 24, 5, 2, 0.3),    # a group that is not full
+    (4100, 136, 40, 20, 4, 0.1),   # three groups, the last of four
+    (4096, 1032, 16, 12, 1, 0.0),  # the smallest batch of this kernel, more than one wave
+    (5000, 72, 8, 3, 2, 0.5),      # four at a time
+    (4095, 136, 16, 12, 2, 0.1),   # the largest of one entry a workgroup
 ])
 def test_large_batches(ep, T, H, E, K, R, empty):  # noqa: F811
     r = Routed(ep, T, E, K, R, hidden=H, empty=empty, seed=T + K)
@@ -69,7 +70,7 @@ def test_large_batches(ep, T, H, E, K, R, empty):  # noqa: F811
         assert torch.isnan(cy[unused.cuda()]).all()
 
 
-@pytest.mark.parametrize("T", [40, 1100])
+@pytest.mark.parametrize("T", [40, 4100])
 def test_first_row_belongs_to_another_token(ep, T):  # noqa: F811
     """Row 0 is named by the last token, in whose place its gradient is
     written, while every other token has empty entries."""
