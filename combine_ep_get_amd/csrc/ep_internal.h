@@ -100,6 +100,10 @@ struct DispatchArgs {
     int32_t nsf, sf_row;
 };
 
+// HIP counts the threads of a launch's dimension in 32 bits; a grid of more is
+// not refused but wraps, so that the last tokens get no workgroup.
+inline bool launch_fits(int64_t workgroups, int64_t threads) { return workgroups * threads < (int64_t{1} << 32); }
+
 constexpr int kCopyThreads = 128;      // dispatch workgroup size
 constexpr int kFusedThreads = 256;     // workgroup of the single-kernel layout + dispatch
 constexpr int kMaxVpt = 8;            // dispatch vectors per thread

@@ -606,6 +606,7 @@ hipError_t launch_expand(const CopyParams &c, const HierParams &h, const Dispatc
                          const int32_t *group_slot, const uint16_t *group_buf, hipStream_t stream) {
     int32_t splits, vpt;
     copy_grid(c.T, c.nvec, kCopyThreads, &splits, &vpt);
+    if (!launch_fits(c.T, kCopyThreads)) return hipErrorInvalidValue;
     CopyParams p = c;
     p.vpt = vpt;
     dim3 grid(c.T, splits, h.G > kNarrowGroups ? 1 : h.G);
@@ -635,6 +636,7 @@ hipError_t launch_group_dispatch(const CopyParams &c, const HierParams &h, const
                                  const int32_t *group_slot, uint16_t *group_buf, hipStream_t stream) {
     int32_t splits, vpt;
     copy_grid(c.T, c.nvec, kCopyThreads, &splits, &vpt);
+    if (!launch_fits(c.T, kCopyThreads)) return hipErrorInvalidValue;
     CopyParams p = c;
     p.vpt = vpt;
     dim3 grid(c.T, splits);
@@ -668,6 +670,7 @@ hipError_t launch_combine_groups(const CopyParams &c, const HierParams &h, const
                                  const int32_t *group_slot, uint16_t *out, hipStream_t stream) {
     int32_t splits, threads;
     combine_grid(c.T, c.nvec, &splits, &threads);
+    if (!launch_fits(c.T, threads)) return hipErrorInvalidValue;
     dim3 grid(c.T, splits);
     // rows in flight per round: all G positions with few groups; with many,
     // the valid rows, of which a token has at most min(G, K)
@@ -695,6 +698,7 @@ hipError_t launch_combine_partial(const CopyParams &c, const HierParams &h, cons
                                   uint16_t *group_buf, hipStream_t stream) {
     int32_t splits, threads;
     combine_grid(c.T, c.nvec, &splits, &threads);
+    if (!launch_fits(c.T, threads)) return hipErrorInvalidValue;
     dim3 grid(c.T, splits);
     const bool wide = h.G > kNarrowGroups;
     const bool stream_rows = stream_group_rows(c, h);

@@ -1120,7 +1120,7 @@ hipError_t launch_layout_dispatch(const LayoutParams &p, const CopyParams &c, co
     cp.vpt = vpt;
     if (!one_chunk && p.T > 0 && p.nchunks <= kMaxCallChunks && p.A == 1) {
         const int64_t blocks = kLeadWorkgroups + static_cast<int64_t>(c.T) * splits;
-        if (blocks > INT32_MAX) return hipErrorInvalidValue;
+        if (!launch_fits(blocks, kCopyThreads)) return hipErrorInvalidValue;
         const dim3 grid(static_cast<uint32_t>(blocks));
         // count pass (with the expert-major arrays), then one launch that
         // finishes the layout and dispatches, each workgroup deriving its

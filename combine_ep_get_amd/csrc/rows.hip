@@ -245,8 +245,7 @@ __global__ __launch_bounds__(kNarrowThreads) void combine_narrow_kernel(
 // 4096 tokens: 197 and 196).
 constexpr int kGradMaxThreads = 512;
 constexpr int kGradTokens = 4096;
-// Tokens of one launch: HIP counts a launch's threads in 32 bits, and a grid
-// of more is not refused but wraps.
+// Tokens of one launch, whose threads have to fit 32 bits.
 constexpr int64_t kGradLaunchTokens = ((int64_t{1} << 32) - 1) / kGradMaxThreads;
 
 template <int KG>
@@ -358,7 +357,7 @@ hipError_t launch_dispatch(const CopyParams &c, const DispatchArgs &a, hipStream
     if (narrow_dispatch(c)) {
         const int64_t n = static_cast<int64_t>(c.T) * c.K * c.nvec;
         const int64_t blocks = (n + kNarrowThreads - 1) / kNarrowThreads;
-        if (blocks > INT32_MAX) return hipErrorInvalidValue;
+        if (!launch_fits(blocks, kNarrowThreads)) return hipErrorInvalidValue;
         dispatch_narrow_kernel<<<static_cast<uint32_t>(blocks), kNarrowThreads, 0, stream>>>(c, a);
         return hipGetLastError();
     }
@@ -370,6 +369,7 @@ hipError_t launch_dispatch(const CopyParams &c, const DispatchArgs &a, hipStream
     copy_grid(c.T, c.nvec, kCopyThreads, &splits, &vpt);
     const bool wide = vpt == 1;
     if (wide) copy_grid(c.T, c.nvec, kFusedThreads, &splits, &vpt);
+    if (!launch_fits(c.T, wide ? kFusedThreads : kCopyThreads)) return hipErrorInvalidValue;
     CopyParams p = c;
     p.vpt = vpt;
     dim3 grid(c.T, splits);
@@ -399,7 +399,7 @@ hipError_t launch_quantize_fp8(int32_t T, int32_t H, const uint16_t *x, uint8_t 
                                hipStream_t stream) {
     const int64_t nblocks = static_cast<int64_t>(T) * (H / 128);
     const int64_t groups = (nblocks + kQuantBlocksPerGroup - 1) / kQuantBlocksPerGroup;
-    if (groups > INT32_MAX) return hipErrorInvalidValue;
+    if (!launch_fits(groups, kQuantThreads)) return hipErrorInvalidValue;
     quantize_fp8_kernel<<<static_cast<uint32_t>(groups), kQuantThreads, 0, stream>>>(nblocks, x, q, sf);
     return hipGetLastError();
 }
@@ -409,7 +409,7 @@ hipError_t launch_combine(const CopyParams &c, const uint16_t *y, const int32_t 
     if (narrow_combine(c)) {
         const int64_t n = static_cast<int64_t>(c.T) * c.nvec;
         const int64_t blocks = (n + kNarrowThreads - 1) / kNarrowThreads;
-        if (blocks > INT32_MAX) return hipErrorInvalidValue;
+        if (!launch_fits(blocks, kNarrowThreads)) return hipErrorInvalidValue;
         const uint32_t g = static_cast<uint32_t>(blocks);
         if (c.K <= 1)
             combine_narrow_kernel<1><<<g, kNarrowThreads, 0, stream>>>(c, y, slot, w, out);
@@ -423,6 +423,7 @@ hipError_t launch_combine(const CopyParams &c, const uint16_t *y, const int32_t 
     }
     int32_t splits, threads;
     combine_grid(c.T, c.nvec, &splits, &threads);
+    if (!launch_fits(c.T, threads)) return hipErrorInvalidValue;
     dim3 grid(c.T, splits);
     if (c.K <= 1) {
         combine_kernel<1><<<grid, threads, 0, stream>>>(y, slot, w, out, c.H, c.K, c.nvec, threads, c.num_rows);
