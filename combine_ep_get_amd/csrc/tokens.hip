@@ -9,11 +9,15 @@
 // tokens, and k is split over the waves of a workgroup in blocks of 128, so
 // that no wave waits for another until the sums are joined in LDS, in a fixed
 // order.  Scaling h by its weight lets the down product sum a token's
-// experts with no further factors.
+// experts with no further factors.  h is rounded to bf16, which the down
+// product's matrix instruction takes; the layer of 128 tokens is off by 0.0023 of
+// its size for it, where the rounding of the result alone gives 0.0017.
 //
 // Measured: one token of top-8 of 64 experts (7168 -> 2 x 2048 -> 7168, 705 MB) 147-156
 // us, 128 tokens of top-8 of 256 (22 GB) 4.4 ms: 4.5-5.1 TB/s, where a large
-// copy reaches 4.7 and a streaming read 5.2.
+// copy reaches 4.7 and a streaming read 5.2.  The down product's workgroups are
+// H / 16: with fewer channels than 2048 they leave CUs idle (64 tokens of 1024
+// channels 2.8 TB/s, of 128 0.5).
 //
 // Every workgroup first sorts the entries by expert in LDS: at most
 // EP_MOE_TOKENS_MAX * EP_MAX_TOPK ids, which stay in L2.  A token that names an
