@@ -99,7 +99,11 @@ extern "C" {
  *   ceil(T / floor(1024 / K)) * round_up(E + R + G + 1, 64) < 2^30 (the
  *   layout's table of per-chunk counts is addressed with 32-bit byte
  *   offsets; this binds only past about 2.6e8 entries at E = 2048,
- *   R = G = 1024, and never at E <= 256 with R <= 64). */
+ *   R = G = 1024, and never at E <= 256 with R <= 64).
+ * Dispatch, combine and the two-level calls also refuse (EP_ERR_HIP) a batch
+ * whose launch would take 2^32 threads or more: a thread takes a 16-byte
+ * vector of a row, or up to eight where rows are long, and a token takes 64
+ * threads (dispatch 128) or more where rows are of 64 vectors or more. */
 typedef struct ep_problem {
     int32_t num_tokens;       /* T: tokens of this source rank */
     int32_t hidden;           /* H: bf16 elements per row, a multiple of 8, <= EP_MAX_HIDDEN */

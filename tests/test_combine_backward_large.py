@@ -33,6 +33,29 @@ def test_more_tokens_than_one_launch_holds(ep):  # noqa: F811
     assert torch.equal(dy.float().cpu(), want_dy)
 
 
+@pytest.mark.parametrize("K", [3, 9])
+@pytest.mark.parametrize("weights", [True, False])
+def test_entries_about_the_end_of_a_launch(ep, K, weights):  # noqa: F811
+    """2^23 + 40 tokens, those around 2^23 with slots: each token's entries, weights and results stay its own."""
+    T, H, n = (1 << 23) + 40, 8, 64
+    first = (1 << 23) - 24
+    g = torch.Generator().manual_seed(K)
+    rows = n * K
+    slot = torch.full((T, K), -1, dtype=torch.int32, device="cuda")
+    slot[first:] = torch.randperm(rows, generator=g).int().view(n, K).cuda()
+    dout, w = torch.zeros(T, H, dtype=torch.bfloat16, device="cuda"), torch.zeros(T, K, device="cuda")
+    d, y, wt = normal(g, n, H), normal(g, rows, H), torch.rand(n, K, generator=g)
+    dout[first:], w[first:] = d.cuda(), wt.cuda()
+    dy, dw = marked(rows, H), torch.full((T, K), 7.0, device="cuda")
+    p = ep.Problem.make(T, H, 16, K, 1, 1, 1, rows)
+    ep.ep_combine_backward(p, dout, y.cuda(), slot, w if weights else None, dy, dw)
+    some = slot[first:].cpu()
+    ok, vy, by, vw, bw = ref.combine_backward(d, y, some, wt if weights else None, rows)
+    ref.assert_within(dy[some[ok].long().cuda()], vy[ok], by[ok], "dy")
+    ref.assert_within(dw[first:], vw, bw, "dweights")
+    assert not dw[:first].any()
+
+
 @pytest.mark.parametrize("T,H,E,K,R,empty", [
     (4200, 264, 32, 8, 4, 0.1),    # eight entries at a time
     (4300, 136, 24, 5, 2, 0.3),    # a group that is not full
