@@ -36,6 +36,12 @@ EP_ACT_SILU = 3
 EP_ACT_SWIGLU = 4
 EP_ACT_GEGLU = 5
 
+EP_SCORE_SOFTMAX = 0
+EP_SCORE_SIGMOID = 1
+
+EP_GRAD_BF16 = 0
+EP_GRAD_FP32 = 1
+
 # Every function the C header declares, checked by the test-suite.
 EXPORTS = ("ep_workspace_bytes", "ep_rank_stride_hint", "ep_get_layout", "ep_dispatch",
            "ep_layout_dispatch", "ep_combine", "ep_quantize_fp8", "ep_dispatch_fp8",
@@ -43,7 +49,10 @@ EXPORTS = ("ep_workspace_bytes", "ep_rank_stride_hint", "ep_get_layout", "ep_dis
            "ep_combine_topk_weights", "ep_read_status", "ep_error_string",
            "ep_layout_dispatch_noalloc", "ep_combine_backward", "ep_expert_product",
            "ep_expert_product_fp8", "ep_product_workspace_bytes", "ep_expert_product_backward",
-           "ep_moe_tokens_workspace_bytes", "ep_moe_tokens", "ep_moe_tokens_fp8")
+           "ep_moe_tokens_workspace_bytes", "ep_moe_tokens", "ep_moe_tokens_fp8",
+           "ep_expert_product_fp4", "ep_moe_tokens_fp4", "ep_route_workspace_bytes", "ep_route",
+           "ep_balance_loss", "ep_route_backward", "ep_grad_workspace_bytes", "ep_grad_square_sum",
+           "ep_grad_clip")
 
 
 class EpError(RuntimeError):
@@ -92,6 +101,62 @@ class Product(ctypes.Structure):
     def weight_rows(self) -> int:
         """M: rows of an expert's weight, both halves of a gated activation."""
         return self.out_features * (2 if self.activation in (EP_ACT_SWIGLU, EP_ACT_GEGLU) else 1)
+
+
+class Router(ctypes.Structure):
+    """``ep_router``: scores, normalisation, the logits' type and the factor of the weights."""
+    _fields_ = [
+        ("score", ctypes.c_int32),
+        ("normalise", ctypes.c_int32),
+        ("logits_bf16", ctypes.c_int32),
+        ("scale", ctypes.c_float),
+    ]
+
+    @classmethod
+    def make(cls, score=EP_SCORE_SOFTMAX, normalise=True, scale=1.0, logits_bf16=False):
+        return cls(score, int(normalise), int(logits_bf16), scale)
+
+
+class Grad(ctypes.Structure):
+    """``ep_grad``: one gradient, and where ep_grad_clip writes it."""
+    _fields_ = [
+        ("grad", ctypes.c_void_p),
+        ("out", ctypes.c_void_p),
+        ("count", ctypes.c_int64),
+        ("type", ctypes.c_int32),
+        ("reserved", ctypes.c_int32),
+    ]
+
+
+class Grads:
+    """The gradients of ep_grad_square_sum and ep_grad_clip, as the host array of ``ep_grad`` that the calls take.
+    It keeps the tensors, whose addresses it holds."""
+
+    def __init__(self, array, tensors):
+        self.array, self.tensors = array, tensors
+
+    def __len__(self) -> int:
+        return len(self.array)
+
+    @classmethod
+    def make(cls, grads, outs=None):
+        """Of bf16 and fp32 tensors, clipped in place unless `outs` names other ones of the same types and sizes."""
+        import torch
+
+        grads = list(grads)
+        outs = grads if outs is None else list(outs)
+        if len(outs) != len(grads):
+            raise ValueError(f"outs: {len(outs)} tensors for {len(grads)} gradients")
+        types = {torch.bfloat16: (EP_GRAD_BF16, "bf16"), torch.float32: (EP_GRAD_FP32, "float")}
+        array = (Grad * len(grads))()
+        for i, (g, o) in enumerate(zip(grads, outs)):
+            if g.dtype not in types or o.dtype != g.dtype:
+                raise ValueError(f"gradient {i}: dtype {g.dtype} into {o.dtype}, expected bfloat16 or float32 in both")
+            if o.numel() != g.numel():
+                raise ValueError(f"outs: tensor {i} has {o.numel()} elements, its gradient {g.numel()}")
+            code, name = types[g.dtype]
+            array[i] = Grad(_arg(g, f"gradient {i}", name, g.numel()), _arg(o, f"out {i}", name, g.numel()), g.numel(), code, 0)
+        return cls(array, (grads, outs))
 
 
 _lib = None
@@ -153,6 +218,25 @@ def load():
         lib.ep_moe_tokens.argtypes = [P, Q] + [vp] * 10 + [sz, vp]
         lib.ep_moe_tokens_fp8.restype = ctypes.c_int
         lib.ep_moe_tokens_fp8.argtypes = [P, Q] + [vp] * 12 + [sz, vp]
+        lib.ep_expert_product_fp4.restype = ctypes.c_int
+        lib.ep_expert_product_fp4.argtypes = [P, Q] + [vp] * 8 + [vp]
+        lib.ep_moe_tokens_fp4.restype = ctypes.c_int
+        lib.ep_moe_tokens_fp4.argtypes = [P, Q] + [vp] * 12 + [sz, vp]
+        RT = ctypes.POINTER(Router)
+        lib.ep_route_workspace_bytes.restype = sz
+        lib.ep_route_workspace_bytes.argtypes = [P, RT]
+        lib.ep_route.restype = ctypes.c_int
+        lib.ep_route.argtypes = [P, RT] + [vp] * 10 + [sz, vp]
+        lib.ep_balance_loss.restype = ctypes.c_int
+        lib.ep_balance_loss.argtypes = [P, RT] + [vp] * 8 + [sz, vp]
+        lib.ep_route_backward.restype = ctypes.c_int
+        lib.ep_route_backward.argtypes = [P, RT] + [vp] * 8 + [vp]
+        lib.ep_grad_workspace_bytes.restype = sz
+        lib.ep_grad_workspace_bytes.argtypes = [vp, ctypes.c_int32]
+        lib.ep_grad_square_sum.restype = ctypes.c_int
+        lib.ep_grad_square_sum.argtypes = [vp, ctypes.c_int32, vp, vp, sz, vp]
+        lib.ep_grad_clip.restype = ctypes.c_int
+        lib.ep_grad_clip.argtypes = [vp, ctypes.c_int32, vp, ctypes.c_float, vp, vp]
         lib.ep_read_status.restype = ctypes.c_int
         lib.ep_read_status.argtypes = [vp, vp]
         lib.ep_error_string.restype = ctypes.c_char_p
@@ -172,6 +256,9 @@ def _dtypes():
         _DTYPES.update({
             "int32": (torch.int32,),
             "int64": (torch.int64,),
+            "double": (torch.float64,),
+            "e2m1": (torch.uint8, torch.int8, torch.float4_e2m1fn_x2),  # two codes a byte
+            "e8m0": (torch.uint8, torch.int8, torch.float8_e8m0fnu),
             "float": (torch.float32,),
             "uint8": (torch.uint8, torch.bool),
             "bf16": (torch.bfloat16, torch.int16, torch.uint16),
@@ -460,8 +547,8 @@ def _product_sizes(problem, product, expert_count):
 
 
 def _product_ref(product, bind):
-    """The product by reference; a bound call keeps a copy of its own."""
-    return ctypes.byref(Product.from_buffer_copy(product) if bind else product)
+    """The product (or router) by reference; a bound call keeps a copy of its own."""
+    return ctypes.byref(type(product).from_buffer_copy(product) if bind else product)
 
 
 def ep_expert_product(problem, product, x, expert_count, expert_offset, weight, bias=None, residual=None, pre=None,
@@ -516,18 +603,22 @@ def ep_moe_tokens_workspace_bytes(problem: Problem, product: Product) -> int:
 
 
 def _tokens_ptrs(problem, product, x, topk_idx, topk_weights, w1, w1_sf, b1, w2, w2_sf, b2, residual, out, workspace,
-                 workspace_bytes, fp8, stream, bind):
+                 workspace_bytes, wtype, stream, bind):
     T, H, K, E, _, _, _ = _sizes(problem)
     I, M = product.out_features, product.weight_rows
-    wtype = "e4m3" if fp8 else "bf16"
     if workspace_bytes is None:
         workspace_bytes = workspace.numel() * workspace.element_size()
-    sf = lambda t, what, n: (_arg(t, what, "float", n),) if fp8 else ()  # noqa: E731
+    codes = 2 if wtype == "e2m1" else 1  # in an element of the weight
+    sf_type, rows, cols = {"bf16": (None, 1, 1), "e4m3": ("float", 128, 128), "e2m1": ("e8m0", 1, 32)}[wtype]
+
+    def sf(t, what, m, c):  # of weight rows m and columns c
+        return (_arg(t, what, sf_type, E * (m // rows) * (c // cols)),) if sf_type else ()
+
     return (_product_ref(product, bind), _arg(x, "x", "bf16", T * H), _arg(topk_idx, "topk_idx", "int32", T * K),
             _arg(topk_weights, "topk_weights", "float", T * K),
-            _arg(w1, "w1", wtype, E * M * H), *sf(w1_sf, "w1_sf", E * (M // 128) * (H // 128)),
+            _arg(w1, "w1", wtype, E * M * H // codes), *sf(w1_sf, "w1_sf", M, H),
             _arg(b1, "b1", "float", E * M),
-            _arg(w2, "w2", wtype, E * H * I), *sf(w2_sf, "w2_sf", E * (H // 128) * (I // 128)),
+            _arg(w2, "w2", wtype, E * H * I // codes), *sf(w2_sf, "w2_sf", H, I),
             _arg(b2, "b2", "float", E * H),
             _arg(residual, "residual", "bf16", T * H), _arg(out, "out", "bf16", T * H),
             _arg(workspace, "workspace", "bytes", workspace_bytes), workspace_bytes, _stream(stream))
@@ -538,14 +629,121 @@ def ep_moe_tokens(problem, product, x, topk_idx, topk_weights, w1, b1, w2, b2, r
     """The whole expert layer for up to EP_MOE_TOKENS_MAX tokens: up product,
     activation, down product, weighted sum and residual, in two kernels."""
     return _run("ep_moe_tokens", problem, _tokens_ptrs(problem, product, x, topk_idx, topk_weights, w1, None, b1, w2,
-        None, b2, residual, out, workspace, workspace_bytes, False, stream, bind), bind)
+        None, b2, residual, out, workspace, workspace_bytes, "bf16", stream, bind), bind)
 
 
 def ep_moe_tokens_fp8(problem, product, x, topk_idx, topk_weights, w1_fp8, w1_sf, b1, w2_fp8, w2_sf, b2, residual, out,
                       workspace, workspace_bytes=None, stream=None, bind=False):
     """ep_moe_tokens with e4m3 weights and one scale for each 128 x 128 of them."""
     return _run("ep_moe_tokens_fp8", problem, _tokens_ptrs(problem, product, x, topk_idx, topk_weights, w1_fp8, w1_sf,
-        b1, w2_fp8, w2_sf, b2, residual, out, workspace, workspace_bytes, True, stream, bind), bind)
+        b1, w2_fp8, w2_sf, b2, residual, out, workspace, workspace_bytes, "e4m3", stream, bind), bind)
+
+
+def ep_expert_product_fp4(problem, product, x, expert_count, expert_offset, w_fp4, w_sf, bias=None, residual=None,
+                          out=None, stream=None, bind=False):
+    """ep_expert_product of up to EP_MOE_TOKENS_MAX tokens with MXFP4 weights:
+    e2m1 codes, two a byte, and one e8m0 scale for each 32 of a row."""
+    E, C, N, M, rows = _product_sizes(problem, product, expert_count)
+    return _run("ep_expert_product_fp4", problem, (_product_ref(product, bind), _arg(x, "x", "bf16", rows * C),
+        _arg(expert_count, "expert_count", "int32", E), _arg(expert_offset, "expert_offset", "int32", E),
+        _arg(w_fp4, "w_fp4", "e2m1", E * M * C // 2), _arg(w_sf, "w_sf", "e8m0", E * M * (C // 32)),
+        _arg(bias, "bias", "float", E * M), _arg(residual, "residual", "bf16", rows * N),
+        _arg(out, "out", "bf16", rows * N), _stream(stream)), bind)
+
+
+def ep_moe_tokens_fp4(problem, product, x, topk_idx, topk_weights, w1_fp4, w1_sf, b1, w2_fp4, w2_sf, b2, residual, out,
+                      workspace, workspace_bytes=None, stream=None, bind=False):
+    """ep_moe_tokens with MXFP4 weights."""
+    return _run("ep_moe_tokens_fp4", problem, _tokens_ptrs(problem, product, x, topk_idx, topk_weights, w1_fp4, w1_sf,
+        b1, w2_fp4, w2_sf, b2, residual, out, workspace, workspace_bytes, "e2m1", stream, bind), bind)
+
+
+def _logits_type(router):
+    return "bf16" if router.logits_bf16 else "float"
+
+
+def _statistics_ptrs(problem, expert_count, token_count, prob_sum, losses, workspace, workspace_bytes):
+    E = problem.num_experts
+    if workspace_bytes is None:
+        workspace_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    return (_arg(expert_count, "expert_count", "int32", E), _arg(token_count, "token_count", "int32", 1),
+            _arg(prob_sum, "prob_sum", "float", E), _arg(losses, "losses", "float", 2),
+            _arg(workspace, "workspace", "bytes", workspace_bytes), workspace_bytes)
+
+
+def ep_route_workspace_bytes(problem: Problem, router: Router) -> int:
+    return load().ep_route_workspace_bytes(ctypes.byref(problem), ctypes.byref(router))
+
+
+def ep_route(problem, router, logits, bias, token_mask, topk_idx, topk_weights, expert_count=None, token_count=None,
+             prob_sum=None, losses=None, workspace=None, workspace_bytes=None, stream=None, bind=False):
+    """The router: top-k experts and their weights from the logits, and with
+    the last arguments the counts, the balance loss and the z loss."""
+    T, _, K, E, _, _, _ = _sizes(problem)
+    return _run("ep_route", problem, (_product_ref(router, bind), _arg(logits, "logits", _logits_type(router), T * E),
+        _arg(bias, "bias", "float", E), _arg(token_mask, "token_mask", "uint8", T),
+        _arg(topk_idx, "topk_idx", "int32", T * K), _arg(topk_weights, "topk_weights", "float", T * K),
+        *_statistics_ptrs(problem, expert_count, token_count, prob_sum, losses, workspace, workspace_bytes),
+        _stream(stream)), bind)
+
+
+def ep_balance_loss(problem, router, logits, topk_idx, token_mask, expert_count, token_count, prob_sum, losses,
+                    workspace, workspace_bytes=None, stream=None, bind=False):
+    """The counts, the balance loss and the z loss of choices made elsewhere."""
+    T, _, K, E, _, _, _ = _sizes(problem)
+    return _run("ep_balance_loss", problem, (_product_ref(router, bind),
+        _arg(logits, "logits", _logits_type(router), T * E), _arg(topk_idx, "topk_idx", "int32", T * K),
+        _arg(token_mask, "token_mask", "uint8", T),
+        *_statistics_ptrs(problem, expert_count, token_count, prob_sum, losses, workspace, workspace_bytes),
+        _stream(stream)), bind)
+
+
+def ep_route_backward(problem, router, logits, topk_idx, token_mask, expert_count, token_count, dweights, dlosses,
+                      dlogits, stream=None, bind=False):
+    """The logits' gradient from those of the weights (None: without) and of
+    the two losses (None: without)."""
+    T, _, K, E, _, _, _ = _sizes(problem)
+    return _run("ep_route_backward", problem, (_product_ref(router, bind),
+        _arg(logits, "logits", _logits_type(router), T * E), _arg(topk_idx, "topk_idx", "int32", T * K),
+        _arg(token_mask, "token_mask", "uint8", T), _arg(expert_count, "expert_count", "int32", E),
+        _arg(token_count, "token_count", "int32", 1), _arg(dweights, "dweights", "float", T * K),
+        _arg(dlosses, "dlosses", "float", 2), _arg(dlogits, "dlogits", _logits_type(router), T * E),
+        _stream(stream)), bind)
+
+
+class _BoundGradCall:
+    """BoundCall for the calls on gradients: holds their array (and so the tensors)."""
+
+    def __init__(self, name: str, grads: Grads, args: tuple):
+        self.name, self.grads = name, grads
+        self._fn, self._args = getattr(load(), name), (grads.array, len(grads), *args)
+
+    def __call__(self) -> int:
+        return _check(self._fn(*self._args), self.name)
+
+
+def _run_grads(name: str, grads: Grads, args: tuple, bind: bool):
+    call = _BoundGradCall(name, grads, args)
+    return call if bind else call()
+
+
+def ep_grad_workspace_bytes(grads: Grads) -> int:
+    return load().ep_grad_workspace_bytes(grads.array, len(grads))
+
+
+def ep_grad_square_sum(grads, square_sum, workspace, workspace_bytes=None, stream=None, bind=False):
+    """square_sum = the sum of all gradients' squares (fp64, on the device);
+    ranks with gradients of their own add theirs up before ep_grad_clip."""
+    if workspace_bytes is None:
+        workspace_bytes = workspace.numel() * workspace.element_size()
+    return _run_grads("ep_grad_square_sum", grads, (_arg(square_sum, "square_sum", "double", 1),
+        _arg(workspace, "workspace", "bytes", workspace_bytes), workspace_bytes, _stream(stream)), bind)
+
+
+def ep_grad_clip(grads, square_sum, max_norm, norm=None, stream=None, bind=False):
+    """out = grad * min(1, max_norm / sqrt(square_sum)), and the norm."""
+    return _run_grads("ep_grad_clip", grads, (_arg(square_sum, "square_sum", "double", 1), max_norm,
+        _arg(norm, "norm", "float", 1), _stream(stream)), bind)
 
 
 def ep_read_status(workspace, stream=None) -> int:

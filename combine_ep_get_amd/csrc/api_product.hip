@@ -73,18 +73,25 @@ int check_tokens(const ep_problem *p, const ep_product *q, int32_t multiple) {
     return EP_OK;
 }
 
+// Multiple that a weight's sizes have to be of: its blocks of one scale.
+int32_t size_step(epget::WeightType w) { return w == epget::kFp8 ? 128 : w == epget::kFp4 ? 32 : 8; }
+
+// Alignment of a weight's scales: fp32, or e8m0 as a whole array.
+uintptr_t scale_alignment(epget::WeightType w) { return w == epget::kFp4 ? 16 : 4; }
+
 int run_tokens(const ep_problem *p, const ep_product *q, const uint16_t *x, const int32_t *topk_idx,
-               const float *topk_weights, const void *w1, const float *w1_sf, const float *b1, const void *w2,
-               const float *w2_sf, const float *b2, const uint16_t *residual, uint16_t *out, void *workspace,
-               size_t workspace_bytes, bool fp8, void *stream) {
-    const int rc = check_tokens(p, q, fp8 ? 128 : 8);
+               const float *topk_weights, const void *w1, const void *w1_sf, const float *b1, const void *w2,
+               const void *w2_sf, const float *b2, const uint16_t *residual, uint16_t *out, void *workspace,
+               size_t workspace_bytes, epget::WeightType type, void *stream) {
+    const int rc = check_tokens(p, q, size_step(type));
     if (rc != EP_OK) return rc;
+    const bool scaled = type != epget::kBf16;
     if (!workspace || !aligned(workspace, 256) || workspace_bytes < static_cast<size_t>(tokens_workspace(p, q)))
         return EP_ERR_INVALID_ARG;
-    if (p->num_tokens > 0 && (!x || !topk_idx || !w1 || !w2 || !out || (fp8 && (!w1_sf || !w2_sf))))
+    if (p->num_tokens > 0 && (!x || !topk_idx || !w1 || !w2 || !out || (scaled && (!w1_sf || !w2_sf))))
         return EP_ERR_INVALID_ARG;
     if (!aligned16(x, w1, b1, w2, b2, residual, out) || !aligned(topk_idx, 4) || !aligned(topk_weights, 4) ||
-        !aligned(w1_sf, 4) || !aligned(w2_sf, 4))
+        !aligned(w1_sf, scale_alignment(type)) || !aligned(w2_sf, scale_alignment(type)))
         return EP_ERR_INVALID_ARG;
     epget::TokensArgs a = {};
     a.T = p->num_tokens;
@@ -107,22 +114,24 @@ int run_tokens(const ep_problem *p, const ep_product *q, const uint16_t *x, cons
     a.out = out;
     a.status = static_cast<int32_t *>(workspace);
     a.h = reinterpret_cast<uint16_t *>(static_cast<char *>(workspace) + 256);
-    return hip_rc(epget::launch_tokens(a, fp8, static_cast<hipStream_t>(stream)));
+    return hip_rc(epget::launch_tokens(a, type, static_cast<hipStream_t>(stream)));
 }
 
 int run_product(const ep_problem *p, const ep_product *q, const void *x, const float *x_sf, int64_t sf_ts,
                 int64_t sf_hs, const int32_t *expert_count, const int32_t *expert_offset, const void *weight,
-                const float *w_sf, const float *bias, const uint16_t *residual, uint16_t *pre, uint16_t *out,
-                bool fp8, void *stream) {
+                const void *w_sf, const float *bias, const uint16_t *residual, uint16_t *pre, uint16_t *out,
+                epget::WeightType type, void *stream) {
     int rc = check_problem(p);
     if (rc != EP_OK) return rc;
-    if ((rc = check_product(q, fp8 ? 128 : 8)) != EP_OK) return rc;
+    if ((rc = check_product(q, size_step(type))) != EP_OK) return rc;
+    const bool fp8 = type == epget::kFp8;
     epget::ProductArgs a = {};
     if ((rc = segments(p, expert_count, expert_offset, &a.seg)) != EP_OK) return rc;
     if (fp8 && (sf_ts < 1 || sf_hs < 1)) return EP_ERR_INVALID_ARG;
     if (p->num_tokens == 0) return EP_OK;
-    if (!x || !weight || !out || (fp8 && (!x_sf || !w_sf))) return EP_ERR_INVALID_ARG;
-    if (!aligned16(x, weight, bias, residual, pre, out) || !aligned(x_sf, 4) || !aligned(w_sf, 4))
+    if (!x || !weight || !out || (fp8 && !x_sf) || (type != epget::kBf16 && !w_sf)) return EP_ERR_INVALID_ARG;
+    if (!aligned16(x, weight, bias, residual, pre, out) || !aligned(x_sf, 4) ||
+        !aligned(w_sf, scale_alignment(type)))
         return EP_ERR_INVALID_ARG;
     a.C = q->in_features;
     a.N = q->out_features;
@@ -140,6 +149,7 @@ int run_product(const ep_problem *p, const ep_product *q, const void *x, const f
     a.out = out;
     a.entries = static_cast<int64_t>(p->num_tokens) * p->num_topk;
     a.mean_rows = mean_rows(p);
+    if (type == epget::kFp4) return hip_rc(epget::launch_product_few(a, type, static_cast<hipStream_t>(stream)));
     return hip_rc(epget::launch_product(a, fp8, static_cast<hipStream_t>(stream)));
 }
 
@@ -170,7 +180,7 @@ int ep_expert_product(const ep_problem *p, const ep_product *q, const uint16_t *
                       const int32_t *expert_offset, const uint16_t *weight, const float *bias,
                       const uint16_t *residual, uint16_t *pre, uint16_t *out, void *stream) {
     return run_product(p, q, x, nullptr, 0, 0, expert_count, expert_offset, weight, nullptr, bias, residual, pre, out,
-                       false, stream);
+                       epget::kBf16, stream);
 }
 
 int ep_expert_product_fp8(const ep_problem *p, const ep_product *q, const uint8_t *x_fp8, const float *x_sf,
@@ -178,7 +188,7 @@ int ep_expert_product_fp8(const ep_problem *p, const ep_product *q, const uint8_
                           const int32_t *expert_offset, const uint8_t *w_fp8, const float *w_sf, const float *bias,
                           const uint16_t *residual, uint16_t *out, void *stream) {
     return run_product(p, q, x_fp8, x_sf, sf_token_stride, sf_hidden_stride, expert_count, expert_offset, w_fp8, w_sf,
-                       bias, residual, nullptr, out, true, stream);
+                       bias, residual, nullptr, out, epget::kFp8, stream);
 }
 
 size_t ep_product_workspace_bytes(const ep_problem *p, const ep_product *q) {
@@ -234,7 +244,7 @@ int ep_moe_tokens(const ep_problem *p, const ep_product *q, const uint16_t *x, c
                   const float *topk_weights, const uint16_t *w1, const float *b1, const uint16_t *w2, const float *b2,
                   const uint16_t *residual, uint16_t *out, void *workspace, size_t workspace_bytes, void *stream) {
     return run_tokens(p, q, x, topk_idx, topk_weights, w1, nullptr, b1, w2, nullptr, b2, residual, out, workspace,
-                      workspace_bytes, false, stream);
+                      workspace_bytes, epget::kBf16, stream);
 }
 
 int ep_moe_tokens_fp8(const ep_problem *p, const ep_product *q, const uint16_t *x, const int32_t *topk_idx,
@@ -242,7 +252,23 @@ int ep_moe_tokens_fp8(const ep_problem *p, const ep_product *q, const uint16_t *
                       const uint8_t *w2_fp8, const float *w2_sf, const float *b2, const uint16_t *residual,
                       uint16_t *out, void *workspace, size_t workspace_bytes, void *stream) {
     return run_tokens(p, q, x, topk_idx, topk_weights, w1_fp8, w1_sf, b1, w2_fp8, w2_sf, b2, residual, out, workspace,
-                      workspace_bytes, true, stream);
+                      workspace_bytes, epget::kFp8, stream);
+}
+
+int ep_expert_product_fp4(const ep_problem *p, const ep_product *q, const uint16_t *x, const int32_t *expert_count,
+                          const int32_t *expert_offset, const uint8_t *w_fp4, const uint8_t *w_sf, const float *bias,
+                          const uint16_t *residual, uint16_t *out, void *stream) {
+    if (p && p->num_tokens > EP_MOE_TOKENS_MAX) return EP_ERR_INVALID_ARG;
+    return run_product(p, q, x, nullptr, 0, 0, expert_count, expert_offset, w_fp4, w_sf, bias, residual, nullptr, out,
+                       epget::kFp4, stream);
+}
+
+int ep_moe_tokens_fp4(const ep_problem *p, const ep_product *q, const uint16_t *x, const int32_t *topk_idx,
+                      const float *topk_weights, const uint8_t *w1_fp4, const uint8_t *w1_sf, const float *b1,
+                      const uint8_t *w2_fp4, const uint8_t *w2_sf, const float *b2, const uint16_t *residual,
+                      uint16_t *out, void *workspace, size_t workspace_bytes, void *stream) {
+    return run_tokens(p, q, x, topk_idx, topk_weights, w1_fp4, w1_sf, b1, w2_fp4, w2_sf, b2, residual, out, workspace,
+                      workspace_bytes, epget::kFp4, stream);
 }
 
 }  // extern "C"

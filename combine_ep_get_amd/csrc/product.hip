@@ -302,7 +302,7 @@ __global__ __launch_bounds__(64 * WF * WT, 2) void product_kernel(Args a) {
             const int kb = a.C / 128;
             // the wave's first output; past N in a tile's unused part
             const int nw = min(n0 + wf * (GATED ? FF * 8 : FF * 16), a.N - 1);
-            sf_w[0] = a.w_sf + (static_cast<int64_t>(e) * (a.M / 128) + nw / 128) * kb;
+            sf_w[0] = static_cast<const float *>(a.w_sf) + (static_cast<int64_t>(e) * (a.M / 128) + nw / 128) * kb;
             sf_w[1] = GATED ? sf_w[0] + static_cast<int64_t>(a.N / 128) * kb : sf_w[0];
         }
         struct Scales {
@@ -717,7 +717,7 @@ bool few_rows(const ProductArgs &a) {
 }
 
 hipError_t launch_product(const ProductArgs &a, bool fp8, hipStream_t stream) {
-    if (few_rows(a)) return launch_product_few(a, fp8, stream);
+    if (few_rows(a)) return launch_product_few(a, fp8 ? kFp8 : kBf16, stream);
     return fp8 ? launch_forward<true>(a, stream) : launch_forward<false>(a, stream);
 }
 

@@ -6,6 +6,9 @@
 
 namespace epget {
 
+// Weights as bf16, as e4m3 with one fp32 scale for 128 x 128, or as e2m1 with one e8m0 scale for 32 of a row.
+enum WeightType { kBf16, kFp8, kFp4 };
+
 // Rows of the experts inside a receive buffer: expert e owns `count[e]` rows
 // from row (e / L) * S + offset[e] on, as the layout places them, cut off at
 // the end of its slice.  Null arrays: one expert that owns rows [0, dense).
@@ -16,13 +19,15 @@ struct Segments {
 };
 
 // One grouped product and its epilogue.  Element sizes: 2 bytes (bf16), or 1
-// (e4m3 codes with scales) for x and the weight of an FP8 product.
+// (e4m3 codes with scales) for x and the weight of an FP8 product, or half a
+// byte (e2m1) for the weight of an FP4 product.
 struct ProductArgs {
     Segments seg;
     int32_t C, N, M;  // inputs, outputs, weight rows (N, or 2N when gated)
     int32_t act;
     const void *x, *weight;
-    const float *x_sf, *w_sf;  // FP8 scales, else null
+    const float *x_sf;         // FP8 scales, else null
+    const void *w_sf;          // fp32 or e8m0 scales, else null
     int64_t sf_ts, sf_hs;
     const float *bias;         // [E, M] or null
     const uint16_t *residual;  // or null
@@ -50,8 +55,8 @@ struct TokensArgs {
     const uint16_t *x;
     const int32_t *idx;
     const float *w;
-    const void *w1, *w2;
-    const float *w1_sf, *w2_sf, *b1, *b2;
+    const void *w1, *w2, *w1_sf, *w2_sf;
+    const float *b1, *b2;
     const uint16_t *residual;
     uint16_t *out;
     int32_t *status;
@@ -62,10 +67,10 @@ struct TokensArgs {
 // the backward call; the bias gradients are summed by range, then joined.
 int32_t grad_row_ranges(int32_t E, int32_t N);
 
-hipError_t launch_product_few(const ProductArgs &a, bool fp8, hipStream_t stream);
+hipError_t launch_product_few(const ProductArgs &a, WeightType w, hipStream_t stream);
 hipError_t launch_product(const ProductArgs &a, bool fp8, hipStream_t stream);
 hipError_t launch_product_grad(const ProductGradArgs &a, hipStream_t stream);
-hipError_t launch_tokens(const TokensArgs &a, bool fp8, hipStream_t stream);
+hipError_t launch_tokens(const TokensArgs &a, WeightType w, hipStream_t stream);
 hipError_t launch_combine_backward(const CopyParams &c, const uint16_t *dout, const uint16_t *y, const int32_t *slot,
                                    const float *w, uint16_t *dy, float *dw, hipStream_t stream);
 

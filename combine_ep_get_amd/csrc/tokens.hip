@@ -101,18 +101,19 @@ constexpr int kWaveItems = 1024;
 
 // This lane's sums of columns c0 .. c0 + 16 CF - 1 of expert e's entries and
 // outputs n0 .. n0 + 15 (of both halves when gated) over a share of k.
-template <bool FP8, int FF, int CF>
+template <int W, int FF, int CF>
 __device__ __forceinline__ void up_columns(const TokensArgs &a, const EntryLists &l, f32x4 (&acc)[FF][CF], int e, int c0,
                                            int m, int s0, int n0, int first, int step) {
     const int li = __lane_id() & 15, lg = __lane_id() >> 4;
-    const int64_t pitch = static_cast<int64_t>(a.H) * (FP8 ? 1 : 2);
+    const int64_t pitch = static_cast<int64_t>(a.H) * weight_bits(W) / 8;
     const char *row[FF], *col[CF];
-    const float *w_sf[FF], *none[CF];
+    const Scale<W> *w_sf[FF];
+    const float *none[CF];
 #pragma unroll
     for (int f = 0; f < FF; ++f) {
         const int64_t r = static_cast<int64_t>(e) * a.M + f * a.I + min(n0 + li, a.I - 1);
         row[f] = static_cast<const char *>(a.w1) + r * pitch;
-        w_sf[f] = FP8 ? a.w1_sf + (static_cast<int64_t>(e) * (a.M / 128) + (f * a.I + n0) / 128) * (a.H / 128) : nullptr;
+        w_sf[f] = weight_scales<W>(a.w1_sf, e, a.M, f * a.I + n0, r, a.H);
     }
 #pragma unroll
     for (int c = 0; c < CF; ++c) {
@@ -122,7 +123,7 @@ __device__ __forceinline__ void up_columns(const TokensArgs &a, const EntryLists
 #pragma unroll
         for (int f = 0; f < FF; ++f) acc[f][c] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     }
-    accumulate_blocks<FP8, false>(acc, row, col, w_sf, none, 0, a.H, first, step, lg);
+    accumulate_blocks<W, false>(acc, row, col, w_sf, none, 0, a.H, first, step, lg);
 }
 
 // h of this lane's column c of the entries and outputs n0 + 4 lg .. + 3.
@@ -148,7 +149,7 @@ __device__ __forceinline__ void up_write(const TokensArgs &a, const EntryLists &
         u32x2{pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3])};
 }
 
-template <int ACT, bool FP8>
+template <int ACT, int W>
 __global__ __launch_bounds__(kFewThreads) void tokens_up_kernel(TokensArgs a) {
     constexpr int FF = act_gated(ACT) ? 2 : 1;
     __shared__ EntryLists l;
@@ -167,14 +168,14 @@ __global__ __launch_bounds__(kFewThreads) void tokens_up_kernel(TokensArgs a) {
         for (int c0 = 0; c0 < m;) {
             if (alone && m - c0 > 16) {
                 f32x4 acc[FF][2];
-                up_columns<FP8, FF, 2>(a, l, acc, e, c0, m, s0, n0, 0, 1);
+                up_columns<W, FF, 2>(a, l, acc, e, c0, m, s0, n0, 0, 1);
                 up_write<ACT>(a, l, e, c0 + li, m, s0, n0, acc[0][0], acc[FF - 1][0]);
                 up_write<ACT>(a, l, e, c0 + 16 + li, m, s0, n0, acc[0][1], acc[FF - 1][1]);
                 c0 += 32;
                 continue;
             }
             f32x4 acc[FF][1];
-            up_columns<FP8, FF, 1>(a, l, acc, e, c0, m, s0, n0, alone ? 0 : wave, alone ? 1 : kFewWaves);
+            up_columns<W, FF, 1>(a, l, acc, e, c0, m, s0, n0, alone ? 0 : wave, alone ? 1 : kFewWaves);
             if (!alone) {
 #pragma unroll
                 for (int f = 0; f < FF; ++f) part[wave][f][lane] = acc[f][0];
@@ -195,20 +196,21 @@ __global__ __launch_bounds__(kFewThreads) void tokens_up_kernel(TokensArgs a) {
 // columns are the expert's entries, and their sums are added to the
 // wave's own sums of every token in LDS, which are joined at the end.  No
 // wave waits for another before that.  sums: [wave][token][16 FF] floats.
-template <bool FP8, int FF, int CF>
+template <int W, int FF, int CF>
 __device__ __forceinline__ void down_columns(const TokensArgs &a, const EntryLists &l, float *sums, int e, int c0, int m,
                                              int s0, int n0, int first, int step) {
     const int lane = __lane_id(), li = lane & 15, lg = lane >> 4;
-    const int64_t pitch = static_cast<int64_t>(a.I) * (FP8 ? 1 : 2);
+    const int64_t pitch = static_cast<int64_t>(a.I) * weight_bits(W) / 8;
     const char *row[FF], *col[CF];
-    const float *w_sf[FF], *none[CF];
+    const Scale<W> *w_sf[FF];
+    const float *none[CF];
     int tok[CF];
     f32x4 acc[FF][CF];
 #pragma unroll
     for (int f = 0; f < FF; ++f) {
-        const int n = min(n0 + f * 16 + li, a.H - 1);
-        row[f] = static_cast<const char *>(a.w2) + (static_cast<int64_t>(e) * a.H + n) * pitch;
-        w_sf[f] = FP8 ? a.w2_sf + (static_cast<int64_t>(e) * (a.H / 128) + min(n0 + f * 16, a.H - 1) / 128) * (a.I / 128) : nullptr;
+        const int64_t r = static_cast<int64_t>(e) * a.H + min(n0 + f * 16 + li, a.H - 1);
+        row[f] = static_cast<const char *>(a.w2) + r * pitch;
+        w_sf[f] = weight_scales<W>(a.w2_sf, e, a.H, min(n0 + f * 16, a.H - 1), r, a.I);
     }
 #pragma unroll
     for (int c = 0; c < CF; ++c) {
@@ -219,7 +221,7 @@ __device__ __forceinline__ void down_columns(const TokensArgs &a, const EntryLis
 #pragma unroll
         for (int f = 0; f < FF; ++f) acc[f][c] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     }
-    accumulate_blocks<FP8, false>(acc, row, col, w_sf, none, 0, a.I, first, step, lg);
+    accumulate_blocks<W, false>(acc, row, col, w_sf, none, 0, a.I, first, step, lg);
 #pragma unroll
     for (int c = 0; c < CF; ++c) {
         if (tok[c] < 0) continue;
@@ -230,7 +232,7 @@ __device__ __forceinline__ void down_columns(const TokensArgs &a, const EntryLis
 
 // MANY: an expert may have more than 16 entries, for which the code takes the registers of
 // a second workgroup on the CU.
-template <bool FP8, int FF, bool MANY>
+template <int W, int FF, bool MANY>
 __global__ __launch_bounds__(kFewThreads, MANY ? 2 : 4) void tokens_down_kernel(TokensArgs a) {
     __shared__ EntryLists l;
     extern __shared__ __attribute__((aligned(16))) float sums[];
@@ -246,9 +248,9 @@ __global__ __launch_bounds__(kFewThreads, MANY ? 2 : 4) void tokens_down_kernel(
         const int s0 = __builtin_amdgcn_readfirstlane(l.start(e)), m = __builtin_amdgcn_readfirstlane(l.end[e]) - s0;
         for (int c0 = 0; c0 < m; c0 += 32) {
             if (!MANY || m - c0 <= 16)
-                down_columns<FP8, FF, 1>(a, l, mine, e, c0, m, s0, n0, u % shares, shares);
+                down_columns<W, FF, 1>(a, l, mine, e, c0, m, s0, n0, u % shares, shares);
             else
-                down_columns<FP8, FF, 2>(a, l, mine, e, c0, m, s0, n0, u % shares, shares);
+                down_columns<W, FF, 2>(a, l, mine, e, c0, m, s0, n0, u % shares, shares);
         }
     }
     __syncthreads();
@@ -274,7 +276,7 @@ __global__ __launch_bounds__(kFewThreads, MANY ? 2 : 4) void tokens_down_kernel(
     }
 }
 
-template <bool FP8>
+template <int W>
 hipError_t launch_up(const TokensArgs &a, hipStream_t stream) {
     const int64_t entries = static_cast<int64_t>(a.T) * a.K;
     const int64_t items = (entries < a.E ? entries : a.E) * ((a.I + 15) / 16);
@@ -282,7 +284,7 @@ hipError_t launch_up(const TokensArgs &a, hipStream_t stream) {
     const uint32_t grid = static_cast<uint32_t>(items < 1 ? 1 : items < kTokenCUs ? items : kTokenCUs);
     switch (a.act) {
 #define EP_ACT_CASE(A) \
-    case A: tokens_up_kernel<A, FP8><<<grid, kFewThreads, 0, stream>>>(a); break;
+    case A: tokens_up_kernel<A, W><<<grid, kFewThreads, 0, stream>>>(a); break;
         EP_ACT_CASE(EP_ACT_NONE)
         EP_ACT_CASE(EP_ACT_RELU)
         EP_ACT_CASE(EP_ACT_GELU)
@@ -295,7 +297,7 @@ hipError_t launch_up(const TokensArgs &a, hipStream_t stream) {
     return hipGetLastError();
 }
 
-template <bool FP8>
+template <int W>
 hipError_t launch_down(const TokensArgs &a, hipStream_t stream) {
     // 32 outputs a workgroup where the tokens' sums leave a CU's LDS to one
     // workgroup or two anyway and 16 would take more than one workgroup a CU,
@@ -307,20 +309,22 @@ hipError_t launch_down(const TokensArgs &a, hipStream_t stream) {
     const uint32_t grid = (a.H + 16 * ff - 1) / (16 * ff), lds = kFewWaves * a.T * 16 * ff * 4;
     static_assert(sizeof(EntryLists) + kFewWaves * EP_MOE_TOKENS_MAX * 16 * 2 * 4 <= 160 * 1024, "a CU's LDS");
     if (ff == 2)
-        tokens_down_kernel<FP8, 2, true><<<grid, kFewThreads, lds, stream>>>(a);
+        tokens_down_kernel<W, 2, true><<<grid, kFewThreads, lds, stream>>>(a);
     else if (a.T > 16)
-        tokens_down_kernel<FP8, 1, true><<<grid, kFewThreads, lds, stream>>>(a);
+        tokens_down_kernel<W, 1, true><<<grid, kFewThreads, lds, stream>>>(a);
     else
-        tokens_down_kernel<FP8, 1, false><<<grid, kFewThreads, lds, stream>>>(a);
+        tokens_down_kernel<W, 1, false><<<grid, kFewThreads, lds, stream>>>(a);
     return hipGetLastError();
 }
 
 }  // namespace
 
-hipError_t launch_tokens(const TokensArgs &a, bool fp8, hipStream_t stream) {
-    const hipError_t rc = fp8 ? launch_up<true>(a, stream) : launch_up<false>(a, stream);
+hipError_t launch_tokens(const TokensArgs &a, WeightType w, hipStream_t stream) {
+    const hipError_t rc = w == kFp4   ? launch_up<kFp4>(a, stream)
+                          : w == kFp8 ? launch_up<kFp8>(a, stream)
+                                      : launch_up<kBf16>(a, stream);
     if (rc != hipSuccess || a.T == 0) return rc;
-    return fp8 ? launch_down<true>(a, stream) : launch_down<false>(a, stream);
+    return w == kFp4 ? launch_down<kFp4>(a, stream) : w == kFp8 ? launch_down<kFp8>(a, stream) : launch_down<kBf16>(a, stream);
 }
 
 }  // namespace epget

@@ -82,11 +82,19 @@ extern "C" {
 #define EP_ACT_SWIGLU 4 /* silu(gate) * up */
 #define EP_ACT_GEGLU 5  /* gelu(gate) * up */
 
+/* Scores of the router. */
+#define EP_SCORE_SOFTMAX 0 /* softmax over the experts */
+#define EP_SCORE_SIGMOID 1 /* 1 / (1 + exp(-logit)) */
+
+/* Element types of a gradient. */
+#define EP_GRAD_BF16 0
+#define EP_GRAD_FP32 1
+
 /* Largest in_features and out_features of an expert product. */
 #define EP_MAX_FEATURES (1 << 16)
 /* Largest number of values of one expert's weight (a 4 GiB bf16 matrix). */
 #define EP_MAX_WEIGHT (INT64_C(1) << 31)
-/* Largest num_tokens of ep_moe_tokens and ep_moe_tokens_fp8. */
+/* Largest num_tokens of the ep_moe_tokens calls and ep_expert_product_fp4. */
 #define EP_MOE_TOKENS_MAX 128
 
 /* Problem description shared by all calls.  Valid when:
@@ -127,6 +135,23 @@ typedef struct ep_product {
     int32_t reserved;     /* must be 0 */
 } ep_product;
 
+/* The router: how logits become choices and weights. */
+typedef struct ep_router {
+    int32_t score;       /* EP_SCORE_* */
+    int32_t normalise;   /* 1: the weights are divided by the sum over the token's choices; else 0 */
+    int32_t logits_bf16; /* element type of logits and dlogits: 1 bf16, 0 fp32 */
+    float scale;         /* factor of the weights, finite */
+} ep_router;
+
+/* One gradient of ep_grad_square_sum and ep_grad_clip. */
+typedef struct ep_grad {
+    const void *grad; /* count values, device, aligned to its elements; may be NULL if count is 0 */
+    void *out;        /* as many of the same type, where ep_grad_clip writes; may be grad */
+    int64_t count;    /* 0 <= count < 2^40 */
+    int32_t type;     /* EP_GRAD_* */
+    int32_t reserved; /* must be 0 */
+} ep_grad;
+
 /* Bytes of device workspace ep_get_layout needs for this problem (chunk
  * count tables and the status word), or 0 if the problem is invalid.  The
  * workspace must be 256-byte aligned; its contents need no initialisation. */
@@ -137,6 +162,81 @@ size_t ep_workspace_bytes(const ep_problem *problem);
  * sizing the buffer from num_max_tokens_per_rank ([SYM] §9.1, §9.5
  * get_buffer_size_hint).  Returns -1 if the problem is otherwise invalid. */
 int64_t ep_rank_stride_hint(const ep_problem *problem);
+
+/* Bytes of device workspace that ep_route (with statistics) and
+ * ep_balance_loss need, or 0 if the problem or router is invalid. */
+size_t ep_route_workspace_bytes(const ep_problem *problem, const ep_router *router);
+
+/* The router, which makes what the layout and the dispatch take.  With the
+ * scores s[t,:] of a token's logits (router->score),
+ *   topk_idx[t,:]     = the K experts of the greatest s[t,e] + bias[e], in
+ *                       descending order, of equal ones the lowest first
+ *   topk_weights[t,j] = scale * s[t,topk_idx[t,j]], with normalise divided by
+ *                       the sum of s over the token's choices
+ * The order is that of the exact scores: without a bias of the logits
+ * themselves, with one of sums in 64 bits.  An expert whose logit is -inf or
+ * NaN, or whose sum is -inf or NaN, is never chosen; an entry that no expert
+ * is left for is -1 with weight 0.  Sums are fp32 or wider; a NaN or +inf
+ * logit makes the softmax of its token NaN, and with it the weights (but not
+ * the normalised ones of other experts), prob_sum and losses.
+ * Only T, E and K of the problem are used; the other fields but S are checked.
+ *
+ *   logits       [T,E] fp32 or bf16 device (router->logits_bf16), 16-byte aligned
+ *   bias         [E] fp32 device, or NULL; in the choice only
+ *   token_mask   [T] uint8 device, or NULL; 0 marks a token that is padding:
+ *                its logits are not read, its entries are -1 with weight 0
+ *   topk_idx     [T,K] int32 device, written
+ *   topk_weights [T,K] fp32 device, written
+ * and, for training, the statistics of the V tokens that count (those that
+ * are no padding and have a logit above -inf), all four or all NULL:
+ *   expert_count [E] int32  choices that name expert e
+ *   token_count  [1] int32  V
+ *   prob_sum     [E] fp32   sum over those tokens of p[t,e], p the softmax of
+ *                           the logits, or the sigmoid divided by its sum
+ *                           over the experts
+ *   losses       [2] fp32   the balance loss E / (K V^2) * sum_e
+ *                           expert_count[e] * prob_sum[e], which is 1 where
+ *                           both are even, and the z loss 1 / V * sum_t
+ *                           logsumexp(logits[t,:])^2; 0 if V is 0
+ *   workspace    ep_route_workspace_bytes bytes, 256-byte aligned; calls that
+ *                may overlap need one each; NULL (with 0 bytes) without
+ *                statistics
+ * Results do not change from call to call. */
+int ep_route(const ep_problem *problem, const ep_router *router, const void *logits,
+             const float *bias, const uint8_t *token_mask, int32_t *topk_idx,
+             float *topk_weights, int32_t *expert_count, int32_t *token_count,
+             float *prob_sum, float *losses, void *workspace, size_t workspace_bytes,
+             void *stream);
+
+/* The statistics and losses of ep_route for choices that were made elsewhere:
+ * topk_idx [T,K] int32 device is read.  Its entries outside [0,E) are empty,
+ * an expert that a token names twice counts twice, and the entries of tokens
+ * that do not count are left out.  router->normalise and scale are checked
+ * but not used. */
+int ep_balance_loss(const ep_problem *problem, const ep_router *router, const void *logits,
+                    const int32_t *topk_idx, const uint8_t *token_mask, int32_t *expert_count,
+                    int32_t *token_count, float *prob_sum, float *losses, void *workspace,
+                    size_t workspace_bytes, void *stream);
+
+/* Gradient of ep_route and ep_balance_loss: dlogits of
+ *   sum_tj dweights[t,j] * topk_weights[t,j] + dlosses[0] * balance loss
+ *   + dlosses[1] * z loss
+ * with the choices and counts taken as constants.  Where several ranks share
+ * the loss of the whole batch, expert_count and token_count are the sums over
+ * the ranks.
+ *
+ *   logits, topk_idx, token_mask  as in the forward call; topk_idx may be
+ *                NULL without dweights; its entries outside [0,E) are empty
+ *   expert_count [E] int32, token_count [1] int32 device, as the forward call
+ *                left them; NULL without dlosses
+ *   dweights     [T,K] fp32 device (what ep_combine_backward gives), or NULL
+ *   dlosses      [2] fp32 device, or NULL
+ *   dlogits      [T,E] of the logits' type, 16-byte aligned, overwritten (0 for
+ *                tokens that do not count); may be logits */
+int ep_route_backward(const ep_problem *problem, const ep_router *router, const void *logits,
+                      const int32_t *topk_idx, const uint8_t *token_mask,
+                      const int32_t *expert_count, const int32_t *token_count,
+                      const float *dweights, const float *dlosses, void *dlogits, void *stream);
 
 /* Routing layout: the counts, prefix sums and per-entry destination slots
  * that [SYM] §6.1 passes to the dispatch kernel (per-scale-up-rank and
@@ -492,8 +592,8 @@ int ep_expert_product_backward(const ep_problem *problem, const ep_product *prod
                                uint16_t *dweight, float *dweight_acc, float *dbias,
                                void *workspace, size_t workspace_bytes, void *stream);
 
-/* Bytes of device workspace that ep_moe_tokens and ep_moe_tokens_fp8 need, or
- * 0 if the problem or product is invalid. */
+/* Bytes of device workspace that the ep_moe_tokens calls need, or 0 if the
+ * problem or product is invalid. */
 size_t ep_moe_tokens_workspace_bytes(const ep_problem *problem, const ep_product *product);
 
 /* The whole expert layer for a few tokens (T <= EP_MOE_TOKENS_MAX), from the
@@ -532,6 +632,58 @@ int ep_moe_tokens_fp8(const ep_problem *problem, const ep_product *product, cons
                       const float *w1_sf, const float *b1, const uint8_t *w2_fp8,
                       const float *w2_sf, const float *b2, const uint16_t *residual,
                       uint16_t *out, void *workspace, size_t workspace_bytes, void *stream);
+
+/* ep_expert_product with 4-bit weights, for a few tokens (T <=
+ * EP_MOE_TOKENS_MAX): the weight is the traffic of a product of few rows, and
+ * this is a quarter of its bf16 bytes.  The format is OCP MXFP4: e2m1 codes
+ * (0, 0.5, 1, 1.5, 2, 3, 4, 6 and, from code 8 on, their negatives) with one
+ * scale byte (e8m0: 2^(byte - 127), 255 is NaN) for each 32 neighbours of a
+ * row.  C and N are multiples of 32.  x stays bf16; a code with its scale is
+ * widened to bf16, which holds it exactly (values below 2^-126 may count as 0).
+ *
+ *   w_fp4 [E,M,C/2] uint8 device, 16-byte aligned; the value of an even c is
+ *         in the low half of its byte
+ *   w_sf  [E,M,C/32] uint8 device, 16-byte aligned
+ *   the others as for ep_expert_product */
+int ep_expert_product_fp4(const ep_problem *problem, const ep_product *product, const uint16_t *x,
+                          const int32_t *expert_count, const int32_t *expert_offset,
+                          const uint8_t *w_fp4, const uint8_t *w_sf, const float *bias,
+                          const uint16_t *residual, uint16_t *out, void *stream);
+
+/* ep_moe_tokens with weights of that format: w1_fp4 [E,M,H/2] with w1_sf
+ * [E,M,H/32], and w2_fp4 [E,H,I/2] with w2_sf [E,H,I/32].  H and I are
+ * multiples of 32. */
+int ep_moe_tokens_fp4(const ep_problem *problem, const ep_product *product, const uint16_t *x,
+                      const int32_t *topk_idx, const float *topk_weights, const uint8_t *w1_fp4,
+                      const uint8_t *w1_sf, const float *b1, const uint8_t *w2_fp4,
+                      const uint8_t *w2_sf, const float *b2, const uint16_t *residual,
+                      uint16_t *out, void *workspace, size_t workspace_bytes, void *stream);
+
+/* Bytes of device workspace that ep_grad_square_sum needs, or 0 if a gradient
+ * is invalid.  `grads` is a host array, of which num_grads may be 0. */
+size_t ep_grad_workspace_bytes(const ep_grad *grads, int32_t num_grads);
+
+/* The global norm of many gradients, and clipping, in two calls, between
+ * which ranks that hold different gradients (the experts') add up theirs:
+ *   square_sum = sum over all gradients of all values squared
+ *   norm       = sqrt(square_sum)
+ *   out        = grad * min(1, max_norm / norm), rounded to its type
+ * Squares and sums are 64-bit, in an order that does not change from call to
+ * call.  Where the norm is not finite nothing is scaled: out = grad, and norm
+ * tells.  A gradient that is its own out and needs no scaling is not touched.
+ * The host array is read during the call and not kept.  Gradients may lie at
+ * any address that their elements allow; no out overlaps another gradient or
+ * out, or its own gradient unless it is the same.
+ *
+ *   square_sum [1] fp64 device, overwritten by the first call
+ *   workspace  ep_grad_workspace_bytes bytes, 256-byte aligned; calls that
+ *              may overlap need one each
+ *   max_norm   >= 0; infinity for no clipping
+ *   norm       [1] fp32 device, written, or NULL */
+int ep_grad_square_sum(const ep_grad *grads, int32_t num_grads, double *square_sum,
+                       void *workspace, size_t workspace_bytes, void *stream);
+int ep_grad_clip(const ep_grad *grads, int32_t num_grads, const double *square_sum,
+                 float max_norm, float *norm, void *stream);
 
 /* Synchronises `stream`, then returns the status word the last
  * ep_get_layout on that workspace wrote (EP_OK, EP_ERR_BAD_EXPERT or

@@ -1,0 +1,219 @@
+"""Products and the few-token layer on MXFP4 weights, on the GPU against their 64-bit forms."""
+import pytest
+import torch
+
+import fp4_reference as fp4
+import product_reference as ref
+from test_moe_tokens import problem, route
+from test_product import Routed, ep, marked, normal, untouched  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+cuda = lambda t: None if t is None else t.cuda()  # noqa: E731
+
+
+def weight(g, E, M, C):
+    return fp4.quantise(torch.randn(E, M, C, generator=g) * C ** -0.5)
+
+
+PRODUCTS = [
+    # T, C, N, E, K, R, A, act, bias, residual
+    (1, 32, 32, 1, 1, 1, 1, "none", False, False),
+    (1, 288, 64, 8, 2, 2, 1, "swiglu", True, True),
+    (5, 96, 160, 4, 2, 1, 4, "geglu", True, False),
+    (17, 256, 32, 3, 3, 1, 1, "silu", False, True),
+    (33, 544, 96, 2, 1, 2, 1, "relu", True, True),
+    (60, 1056, 32, 5, 2, 1, 8, "gelu", True, True),
+    (64, 2080, 96, 16, 4, 4, 1, "swiglu", False, False),
+    (100, 320, 416, 32, 4, 4, 1, "none", True, True),
+    (128, 512, 64, 2, 2, 1, 1, "swiglu", True, True),
+    (128, 64, 2048, 300, 8, 2, 1, "silu", False, False),
+]
+
+
+@pytest.mark.parametrize("case", PRODUCTS, ids=lambda c: "-".join(map(str, c)))
+def test_product(ep, case):  # noqa: F811
+    T, C, N, E, K, R, A, act, bias, residual = case
+    g = torch.Generator().manual_seed(T + C)
+    r = Routed(ep, T, E, K, R, A, empty=0.1 if T > 4 else 0.0, hot=T > 30)
+    q = ep.Product.make(C, N, ref.ACTS.index(act))
+    M = q.weight_rows
+    x, (w, sf) = normal(g, r.rows, C), weight(g, E, M, C)
+    b = torch.randn(E, M, generator=g) if bias else None
+    res = normal(g, r.rows, N) if residual else None
+    out = marked(r.rows, N)
+    ep.ep_expert_product_fp4(r.p, q, cuda(x), *r.arrays, cuda(w), cuda(sf), cuda(b), cuda(res), out)
+    for e, rows in r.of.items():
+        if rows:
+            o, bound, _, _ = ref.product(act, x[rows], fp4.values(w[e], sf[e]), None if b is None else b[e],
+                                         None if res is None else res[rows])
+            ref.assert_within(out[rows], o, bound, f"expert {e}")
+    assert untouched(out, r.used)
+    if residual:  # into the residual itself: the same bits
+        again = cuda(res)
+        ep.ep_expert_product_fp4(r.p, q, cuda(x), *r.arrays, cuda(w), cuda(sf), cuda(b), again, again)
+        assert torch.equal(again[r.used].view(torch.int16), out[r.used].view(torch.int16))
+
+
+@pytest.mark.parametrize("T", [1, 2, 15, 16, 17, 37, 64, 65, 128])
+@pytest.mark.parametrize("C,N", [(32, 8192), (7168, 32), (4096, 256), (96, 96), (1408, 1184)])
+def test_dense_product(ep, T, C, N):  # noqa: F811
+    """One weight for all rows: a matrix-vector product at T = 1."""
+    g = torch.Generator().manual_seed(T * 7 + C)
+    p, q = ep.Problem.make(T, 64, 1, 1, 1, 1, 1, T), ep.Product.make(C, N, ep.EP_ACT_SWIGLU)
+    x, (w, sf) = normal(g, T, C), weight(g, 1, 2 * N, C)
+    out = marked(T + 1, N)
+    ep.ep_expert_product_fp4(p, q, cuda(x), None, None, cuda(w), cuda(sf), None, None, out)
+    o, bound, _, _ = ref.product("swiglu", x, fp4.values(w[0], sf[0]))
+    ref.assert_within(out[:T], o, bound)
+    assert untouched(out, list(range(T)))
+
+
+def test_every_code_and_scale(ep):  # noqa: F811
+    """Rows that pick one column each read the weight's values exactly: all codes with all scales whose values bf16
+    holds as normal numbers, and NaN for the scale 255."""
+    C, N = 128, 16 * 64
+    sf = torch.arange(N * C // 32, dtype=torch.int64).view(N, C // 32)
+    sf = (2 + sf % 250).to(torch.uint8)
+    codes = ((torch.arange(N * C // 2).view(N, C // 2) * 37) % 256).to(torch.uint8)
+    want = fp4.values(codes, sf)
+    p, q = ep.Problem.make(C, 64, 1, 1, 1, 1, 1, C), ep.Product.make(C, N)
+    x = torch.eye(C).bfloat16().cuda()
+    out = marked(C, N)
+    ep.ep_expert_product_fp4(p, q, x, None, None, codes.cuda(), sf.cuda(), None, None, out)
+    got = out.cpu().double().t()
+    assert torch.equal(got, want)
+    assert len(set(zip(codes.flatten().tolist(), sf.repeat_interleave(16, 1).flatten().tolist()))) > 8000
+    sf[5, 1] = 255
+    ep.ep_expert_product_fp4(p, q, x, None, None, codes.cuda(), sf.cuda(), None, None, out)
+    got = out.cpu().double().t()
+    assert torch.isnan(got[5]).all()  # every row's sum runs over the NaN
+    got[5], want[5] = 0, 0
+    assert torch.equal(got, want)
+
+
+def test_smallest_scales(ep):  # noqa: F811
+    """Values below the normal numbers come out exactly or as zero."""
+    C, N = 32, 32
+    sf = (torch.arange(N) % 4).to(torch.uint8).view(N, 1)
+    codes = torch.full((N, C // 2), 0x72, dtype=torch.uint8)
+    want = fp4.values(codes, sf)
+    p, q = ep.Problem.make(C, 64, 1, 1, 1, 1, 1, C), ep.Product.make(C, N)
+    out = marked(C, N)
+    ep.ep_expert_product_fp4(p, q, torch.eye(C).bfloat16().cuda(), None, None, codes.cuda(), sf.cuda(), None, None, out)
+    got = out.cpu().double().t()
+    assert (((got == want) | ((got == 0) & (want < 2.0 ** -126)))).all()
+
+
+TOKENS = [
+    # T, H, I, E, K, act, bias, residual, weights, twice, empty
+    (1, 32, 32, 1, 1, "none", False, False, False, False, 0.0),
+    (1, 288, 160, 16, 4, "swiglu", True, True, True, False, 0.0),
+    (3, 96, 224, 4, 2, "geglu", False, True, True, True, 0.2),
+    (16, 544, 64, 8, 3, "silu", True, False, True, False, 0.0),
+    (17, 160, 288, 5, 5, "gelu", True, True, False, False, 0.1),
+    (50, 256, 128, 3, 2, "relu", False, False, True, True, 0.0),
+    (90, 352, 96, 64, 8, "swiglu", True, True, True, False, 0.1),
+    (128, 64, 64, 2, 2, "swiglu", False, True, True, False, 0.0),
+    (128, 64, 32, 300, 32, "geglu", True, True, True, True, 0.1),
+    (100, 4128, 32, 2, 2, "silu", False, False, True, False, 0.0),   # 32 outputs a workgroup of the down product
+    (2, 1056, 1312, 8, 8, "swiglu", False, True, True, False, 0.0),
+]
+
+
+@pytest.mark.parametrize("case", TOKENS, ids=lambda c: "-".join(map(str, c[:6])))
+def test_tokens(ep, case):  # noqa: F811
+    T, H, I, E, K, act, bias, residual, weights, twice, empty = case
+    g = torch.Generator().manual_seed(T)
+    idx = route(g, T, E, K, empty, twice)
+    p, q = problem(ep, T, H, E, K), ep.Product.make(H, I, ref.ACTS.index(act))
+    M = q.weight_rows
+    x, (w1, s1), (w2, s2) = normal(g, T, H), weight(g, E, M, H), weight(g, E, H, I)
+    b1, b2 = (torch.randn(E, M, generator=g), torch.randn(E, H, generator=g)) if bias else (None, None)
+    res = normal(g, T, H) if residual else None
+    tw = torch.rand(T, K, generator=g) if weights else None
+    ws = torch.empty(ep.ep_moe_tokens_workspace_bytes(p, q), dtype=torch.uint8, device="cuda")
+    out = marked(T + 1, H)
+    d = [cuda(t) for t in (x, idx, tw, w1, s1, b1, w2, s2, b2, res)]
+    ep.ep_moe_tokens_fp4(p, q, *d, out, ws)
+    assert ep.ep_read_status(ws) == ep.EP_OK
+    want, bound = ref.tokens(act, x, idx, tw, fp4.values(w1, s1), b1, fp4.values(w2, s2), b2, res)
+    ref.assert_within(out[:T], want, bound)
+    assert untouched(out, list(range(T)))
+    again = d[0].clone()  # into x itself: the same bits
+    ep.ep_moe_tokens_fp4(p, q, again, *d[1:], again, ws)
+    assert torch.equal(again.view(torch.int16), out[:T].view(torch.int16))
+
+
+def small(ep, T=6, E=4, K=2, H=96, I=64):  # noqa: F811
+    g = torch.Generator().manual_seed(2)
+    p, q = problem(ep, T, H, E, K), ep.Product.make(H, I, ep.EP_ACT_SILU)
+    x, w1, w2 = normal(g, T, H).cuda(), [t.cuda() for t in weight(g, E, I, H)], [t.cuda() for t in weight(g, E, H, I)]
+    idx, tw = route(g, T, E, K).cuda(), torch.rand(T, K, generator=g).cuda()
+    ws = torch.empty(ep.ep_moe_tokens_workspace_bytes(p, q), dtype=torch.uint8, device="cuda")
+    return p, q, x, idx, tw, w1, w2, ws
+
+
+def test_bad_ids_and_no_tokens(ep):  # noqa: F811
+    p, q, x, idx, tw, w1, w2, ws = small(ep)
+    want, out = marked(*x.shape), marked(*x.shape)
+    idx[2, 1] = -1
+    ep.ep_moe_tokens_fp4(p, q, x, idx, tw, *w1, None, *w2, None, None, want, ws)
+    assert ep.ep_read_status(ws) == ep.EP_OK
+    idx[2, 1] = 4
+    ep.ep_moe_tokens_fp4(p, q, x, idx, tw, *w1, None, *w2, None, None, out, ws)
+    assert ep.ep_read_status(ws) == ep.EP_ERR_BAD_EXPERT and torch.equal(out, want)
+    idx.fill_(-1)
+    ep.ep_moe_tokens_fp4(p, q, x, idx, tw, *w1, None, *w2, None, x, out, ws)
+    assert torch.equal(out, x)
+    p.num_tokens = 0
+    out = marked(1, 96)
+    ep.ep_moe_tokens_fp4(p, q, x, idx, tw, *w1, None, *w2, None, None, out, ws)
+    assert untouched(out, [])
+    ep.ep_expert_product_fp4(p, q, x, idx, idx, *w1, None, None, out)
+    assert untouched(out, [])
+
+
+def test_values_that_are_not_finite_stay_with_their_tokens(ep):  # noqa: F811
+    p, q, x, idx, tw, w1, w2, ws = small(ep, T=40, E=8)
+    clean, out = marked(*x.shape), marked(*x.shape)
+    ep.ep_moe_tokens_fp4(p, q, x, idx, tw, *w1, None, *w2, None, None, clean, ws)
+    x[5, 3] = float("nan")
+    w1[1][6, 2] = 255
+    ep.ep_moe_tokens_fp4(p, q, x, idx, tw, *w1, None, *w2, None, None, out, ws)
+    hit = (idx == 6).any(1)
+    hit[5] = True
+    assert torch.isnan(out[hit]).all() and 0 < int(hit.sum()) < 40
+    assert torch.equal(out[~hit], clean[~hit])
+
+
+def test_other_types_of_the_same_bytes(ep):  # noqa: F811
+    p, q, x, idx, tw, w1, w2, ws = small(ep)
+    want, out = marked(*x.shape), marked(*x.shape)
+    ep.ep_moe_tokens_fp4(p, q, x, idx, tw, *w1, None, *w2, None, None, want, ws)
+    as_types = lambda w: (w[0].view(torch.float4_e2m1fn_x2), w[1].view(torch.float8_e8m0fnu))  # noqa: E731
+    ep.ep_moe_tokens_fp4(p, q, x, idx, tw, *as_types(w1), None, *as_types(w2), None, None, out, ws)
+    assert torch.equal(out, want)
+
+
+def test_graph_replays(ep):  # noqa: F811
+    p, q, x, idx, tw, w1, w2, ws = small(ep, T=20, E=8)
+    batches = [idx.clone(), idx.flip(0).contiguous()]
+    want = []
+    for i in batches:
+        o = marked(*x.shape)
+        ep.ep_moe_tokens_fp4(p, q, x, i, tw, *w1, None, *w2, None, x, o, ws)
+        want.append(o)
+    outs, graphs, spaces = [marked(*x.shape) for _ in range(2)], [], [ws, ws.clone()]
+    torch.cuda.synchronize()
+    for o, s in zip(outs, spaces):
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            ep.ep_moe_tokens_fp4(p, q, x, idx, tw, *w1, None, *w2, None, x, o, s)
+    for n in range(4):
+        idx.copy_(batches[n % 2])
+        for o, gr in zip(outs, graphs):
+            o.zero_()
+            gr.replay()
+        torch.cuda.synchronize()
+        for o in outs:
+            assert torch.equal(o, want[n % 2])
