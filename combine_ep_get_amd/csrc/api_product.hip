@@ -114,7 +114,8 @@ int run_tokens(const ep_problem *p, const ep_product *q, const uint16_t *x, cons
     a.out = out;
     a.status = static_cast<int32_t *>(workspace);
     a.h = reinterpret_cast<uint16_t *>(static_cast<char *>(workspace) + 256);
-    return hip_rc(epget::launch_tokens(a, type, static_cast<hipStream_t>(stream)));
+    if (type == epget::kFp4) return hip_rc(epget::launch_tokens_fp4(a, static_cast<hipStream_t>(stream)));
+    return hip_rc(epget::launch_tokens(a, type == epget::kFp8, static_cast<hipStream_t>(stream)));
 }
 
 int run_product(const ep_problem *p, const ep_product *q, const void *x, const float *x_sf, int64_t sf_ts,
@@ -149,7 +150,7 @@ int run_product(const ep_problem *p, const ep_product *q, const void *x, const f
     a.out = out;
     a.entries = static_cast<int64_t>(p->num_tokens) * p->num_topk;
     a.mean_rows = mean_rows(p);
-    if (type == epget::kFp4) return hip_rc(epget::launch_product_few(a, type, static_cast<hipStream_t>(stream)));
+    if (type == epget::kFp4) return hip_rc(epget::launch_product_fp4(a, static_cast<hipStream_t>(stream)));
     return hip_rc(epget::launch_product(a, fp8, static_cast<hipStream_t>(stream)));
 }
 

@@ -13,7 +13,7 @@
 namespace epget {
 namespace {
 
-template <int ACT, int W>
+template <int ACT, bool FP8>
 __global__ __launch_bounds__(kFewThreads) void product_few_kernel(ProductArgs a) {
     constexpr bool GATED = act_gated(ACT);
     constexpr int FF = GATED ? 2 : 1;
@@ -31,7 +31,7 @@ __global__ __launch_bounds__(kFewThreads) void product_few_kernel(ProductArgs a)
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int nf = (a.N + 15) / 16;
     const int64_t total = static_cast<int64_t>(first[a.seg.E]) * nf;
-    const int64_t pitch = static_cast<int64_t>(a.C) * weight_bits(W) / 8;
+    const int64_t pitch = static_cast<int64_t>(a.C) * (FP8 ? 1 : 2);
     const int G = gridDim.x;
     for (int64_t round = 0; round * G < total; ++round) {
         const int64_t tile = tile_of(total, round, blockIdx.x, G);
@@ -45,21 +45,21 @@ __global__ __launch_bounds__(kFewThreads) void product_few_kernel(ProductArgs a)
         const int rows = segment(a.seg, e, &row0);
         const int n0 = ft * 16, t0 = tt * 16;
         const char *row[FF];
-        const Scale<W> *w_sf[FF];
+        const float *w_sf[FF];
         f32x4 acc[FF][1];
 #pragma unroll
         for (int f = 0; f < FF; ++f) {
             const int64_t r = static_cast<int64_t>(e) * a.M + f * a.N + min(n0 + li, a.N - 1);
             row[f] = static_cast<const char *>(a.weight) + r * pitch;
-            w_sf[f] = weight_scales<W>(a.w_sf, e, a.M, f * a.N + n0, r, a.C);
+            w_sf[f] = FP8 ? static_cast<const float *>(a.w_sf) + (static_cast<int64_t>(e) * (a.M / 128) + (f * a.N + n0) / 128) * (a.C / 128) : nullptr;
             acc[f][0] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
         }
         const int64_t xr = row0 + min(t0 + li, rows - 1);
-        const char *const col[1] = {static_cast<const char *>(a.x) + xr * a.C * (W == kFp8 ? 1 : 2)};
-        const float *const x_sf[1] = {W == kFp8 ? a.x_sf + xr * a.sf_ts : nullptr};
+        const char *const col[1] = {static_cast<const char *>(a.x) + xr * pitch};
+        const float *const x_sf[1] = {FP8 ? a.x_sf + xr * a.sf_ts : nullptr};
         // neighbouring tiles start at different blocks of k, so that they do
         // not all read the same piece of x at once (1.5 us of 14)
-        accumulate_blocks<W, W == kFp8>(acc, row, col, w_sf, x_sf, a.sf_hs, a.C, (wave + ft) % kFewWaves, kFewWaves, lg);
+        accumulate_blocks<FP8, FP8>(acc, row, col, w_sf, x_sf, a.sf_hs, a.C, (wave + ft) % kFewWaves, kFewWaves, lg);
         const int tok = t0 + li, n = n0 + lg * 4;
 #pragma unroll
         for (int f = 0; f < FF; ++f) part[wave][f][lane] = acc[f][0];
@@ -73,22 +73,21 @@ __global__ __launch_bounds__(kFewThreads) void product_few_kernel(ProductArgs a)
     }
 }
 
-template <int ACT, int W>
+template <int ACT, bool FP8>
 hipError_t launch_few(const ProductArgs &a, hipStream_t stream) {
     // no more workgroups than tiles there can be, each expert's last tile in part filled
     const int64_t tiles = (a.entries / 16 + min(static_cast<int64_t>(a.seg.E), a.entries)) * ((a.N + 15) / 16);
     const uint32_t grid = static_cast<uint32_t>(min(int64_t{512}, (tiles + 7) / 8 * 8));
-    product_few_kernel<ACT, W><<<grid, kFewThreads, 0, stream>>>(a);
+    product_few_kernel<ACT, FP8><<<grid, kFewThreads, 0, stream>>>(a);
     return hipGetLastError();
 }
 
 }  // namespace
 
-hipError_t launch_product_few(const ProductArgs &a, WeightType w, hipStream_t stream) {
+hipError_t launch_product_few(const ProductArgs &a, bool fp8, hipStream_t stream) {
     switch (a.act) {
 #define EP_ACT_CASE(A) \
-    case A:            \
-        return w == kFp4 ? launch_few<A, kFp4>(a, stream) : w == kFp8 ? launch_few<A, kFp8>(a, stream) : launch_few<A, kBf16>(a, stream);
+    case A: return fp8 ? launch_few<A, true>(a, stream) : launch_few<A, false>(a, stream);
         EP_ACT_CASE(EP_ACT_NONE)
         EP_ACT_CASE(EP_ACT_RELU)
         EP_ACT_CASE(EP_ACT_GELU)

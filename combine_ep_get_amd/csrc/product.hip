@@ -717,7 +717,7 @@ bool few_rows(const ProductArgs &a) {
 }
 
 hipError_t launch_product(const ProductArgs &a, bool fp8, hipStream_t stream) {
-    if (few_rows(a)) return launch_product_few(a, fp8 ? kFp8 : kBf16, stream);
+    if (few_rows(a)) return launch_product_few(a, fp8, stream);
     return fp8 ? launch_forward<true>(a, stream) : launch_forward<false>(a, stream);
 }
 

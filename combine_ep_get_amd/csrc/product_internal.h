@@ -67,10 +67,12 @@ struct TokensArgs {
 // the backward call; the bias gradients are summed by range, then joined.
 int32_t grad_row_ranges(int32_t E, int32_t N);
 
-hipError_t launch_product_few(const ProductArgs &a, WeightType w, hipStream_t stream);
+hipError_t launch_product_few(const ProductArgs &a, bool fp8, hipStream_t stream);
 hipError_t launch_product(const ProductArgs &a, bool fp8, hipStream_t stream);
 hipError_t launch_product_grad(const ProductGradArgs &a, hipStream_t stream);
-hipError_t launch_tokens(const TokensArgs &a, WeightType w, hipStream_t stream);
+hipError_t launch_tokens(const TokensArgs &a, bool fp8, hipStream_t stream);
+hipError_t launch_product_fp4(const ProductArgs &a, hipStream_t stream);
+hipError_t launch_tokens_fp4(const TokensArgs &a, hipStream_t stream);
 hipError_t launch_combine_backward(const CopyParams &c, const uint16_t *dout, const uint16_t *y, const int32_t *slot,
                                    const float *w, uint16_t *dy, float *dw, hipStream_t stream);
 

@@ -217,3 +217,23 @@ def test_graph_replays(ep):  # noqa: F811
         torch.cuda.synchronize()
         for o in outs:
             assert torch.equal(o, want[n % 2])
+
+
+@pytest.mark.parametrize("T,E", [(128, 1), (128, 2), (100, 5), (60, 4)])
+def test_many_tokens_an_expert(ep, T, E):  # noqa: F811
+    """An expert's tokens fill many tiles, which different workgroups take."""
+    H, I, K = 64, 1024, 1
+    g = torch.Generator().manual_seed(T + E)
+    idx = torch.randint(0, E, (T, K), generator=g).int()
+    p, q = problem(ep, T, H, E, K), ep.Product.make(H, I, ep.EP_ACT_NONE)
+    x, (w1, s1), (w2, s2) = normal(g, T, H), weight(g, E, I, H), weight(g, E, H, I)
+    ws = torch.empty(ep.ep_moe_tokens_workspace_bytes(p, q), dtype=torch.uint8, device="cuda")
+    want, bound = ref.tokens("none", x, idx, None, fp4.values(w1, s1), None, fp4.values(w2, s2), None, None)
+    first = None
+    for _ in range(5):
+        ws.fill_(255)
+        out = marked(T, H)
+        ep.ep_moe_tokens_fp4(p, q, cuda(x), cuda(idx), None, cuda(w1), cuda(s1), None, cuda(w2), cuda(s2), None, None, out, ws)
+        ref.assert_within(out, want, bound)
+        first = out if first is None else first
+        assert torch.equal(out.view(torch.int16), first.view(torch.int16))
