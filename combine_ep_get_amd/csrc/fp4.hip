@@ -19,6 +19,8 @@
 // pieces of a line are permuted there by bits of the row, on the side of the
 // load's address, so that neither the writes, linear, nor the reads have
 // bank conflicts.
+#include <limits.h>
+
 #include "tokens_device.h"
 
 namespace epget {
@@ -300,57 +302,112 @@ __global__ __launch_bounds__(kFewThreads, 2) void product_fp4_kernel(ProductArgs
     }
 }
 
-// The lists of sort_entries, in LDS that the launch sizes, and the tiles of
-// entries: `first` holds those of the experts (with entries) before each.
+// The entries by expert and their tiles, in LDS that the launch sizes.
 struct Lists {
-    int *end, *first, *wave_sum;
-    uint16_t *expert, *entry, *ordered;
-    int16_t *id;
+    int *end;                  // sort_entries' (by expert)
+    int *begin, *first;        // entries and tiles of the experts (with entries) before each
+    int *wave_sum;
+    uint16_t *expert, *entry;  // the experts, ascending, and the entries by expert
+    uint16_t *owner;           // number in `expert` of each tile
+    uint16_t *ordered;
+    int16_t *id;               // expert of each entry, -1 for none
     int &experts, &bad;
 
     static __host__ __device__ int most(const TokensArgs &a) { return a.E < a.T * a.K ? a.E : a.T * a.K; }
     static __host__ __device__ int bytes(const TokensArgs &a) {
-        return (a.E * 4 + (most(a) + 1) * 4 + (kFewWaves + 2) * 4 + most(a) * 2 + a.T * a.K * 6 + 15) / 16 * 16;
+        return (a.E * 4 + (most(a) + 1) * 8 + (kFewWaves + 2) * 4 + most(a) * 2 + a.T * a.K * 8 + 15) / 16 * 16;
     }
     __device__ __forceinline__ Lists(const TokensArgs &a, char *p)
-        : end(reinterpret_cast<int *>(p)), first(end + a.E), wave_sum(first + most(a) + 1),
-          expert(reinterpret_cast<uint16_t *>(wave_sum + kFewWaves + 2)), entry(expert + most(a)),
-          ordered(entry + a.T * a.K), id(reinterpret_cast<int16_t *>(ordered + a.T * a.K)), experts(wave_sum[kFewWaves]), bad(wave_sum[kFewWaves + 1]) {}
-    __device__ __forceinline__ int start(int e) const { return e ? end[e - 1] : 0; }
+        : end(reinterpret_cast<int *>(p)), begin(end + a.E), first(begin + most(a) + 1), wave_sum(first + most(a) + 1),
+          expert(reinterpret_cast<uint16_t *>(wave_sum + kFewWaves + 2)), entry(expert + most(a)), owner(entry + a.T * a.K),
+          ordered(owner + a.T * a.K), id(reinterpret_cast<int16_t *>(ordered + a.T * a.K)), experts(wave_sum[kFewWaves]),
+          bad(wave_sum[kFewWaves + 1]) {}
 
-    // Entries of an expert in ascending order, where more than one workgroup takes tiles of them: the sort leaves
-    // them in the order of its atomics, which another workgroup does not share.  Followed by a barrier (in tiles).
-    template <int NT>
-    __device__ __forceinline__ void order() {
-        const int n = experts ? end[expert[experts - 1]] : 0;
-        for (int p = threadIdx.x; p < n; p += NT) {
-            const int v = entry[p], e = id[v], s = start(e), m = end[e] - s;
-            int rank = 0;
-            for (int q = s; q < s + m; ++q) rank += entry[q] < v;
-            ordered[s + rank] = static_cast<uint16_t>(v);
+    // Fills them, tiles being of `width` entries at most.  ORDER: an expert's entries lie in ascending order, which they
+    // have to where several workgroups take tiles of them.  Called by the whole workgroup; ends with a barrier.
+    template <int NT, bool ORDER>
+    __device__ __forceinline__ void fill(const TokensArgs &a, int width) {
+        if (a.T * a.K <= 64) {
+            if (threadIdx.x < 64) fill_wave(a, width);
+            __syncthreads();
+            return;
         }
-        entry = ordered;
-    }
-
-    // Called by the whole workgroup after sort_entries; ends with a barrier.
-    template <int NT>
-    __device__ __forceinline__ void tiles(int width) {
+        sort_entries<NT>(a, *this);
         const int per = (experts + NT - 1) / NT;
         const int i0 = min(static_cast<int>(threadIdx.x) * per, experts), i1 = min(i0 + per, experts);
+        auto start = [&](int e) { return e ? end[e - 1] : 0; };
         int sum = 0;
         for (int i = i0; i < i1; ++i) sum += (end[expert[i]] - start(expert[i]) + width - 1) / width;
         const int incl = wave_inclusive_sum(sum);
         if ((threadIdx.x & 63) == 63) wave_sum[threadIdx.x >> 6] = incl;
+        const int n = experts ? end[expert[experts - 1]] : 0;
+        if (ORDER) {  // the sort leaves an expert's entries in the order of its atomics
+            for (int p = threadIdx.x; p < n; p += NT) {
+                const int v = entry[p], e = id[v], s = start(e), m = end[e] - s;
+                int rank = p - s;
+                if (m > width) {
+                    rank = 0;
+                    for (int q = s; q < s + m; ++q) rank += entry[q] < v;
+                }
+                ordered[s + rank] = static_cast<uint16_t>(v);
+            }
+            entry = ordered;
+        }
         __syncthreads();
         int before = incl - sum;
         for (int w = 0; w < NT / 64; ++w)
             if (w < static_cast<int>(threadIdx.x >> 6)) before += wave_sum[w];
         for (int i = i0; i < i1; ++i) {
+            begin[i] = start(expert[i]);
             first[i] = before;
-            before += (end[expert[i]] - start(expert[i]) + width - 1) / width;
+            for (int m = end[expert[i]] - begin[i]; m > 0; m -= width) owner[before++] = static_cast<uint16_t>(i);
         }
-        if (threadIdx.x == NT - 1) first[experts] = before;
+        if (threadIdx.x == NT - 1) first[experts] = before, begin[experts] = n;
         __syncthreads();
+    }
+
+    // The same for up to 64 entries, one a lane of one wave: a decode batch waits for no other wave (5 us less on a layer
+    // of one token).
+    __device__ __forceinline__ void fill_wave(const TokensArgs &a, int width) {
+        const int i = threadIdx.x, n = a.T * a.K;
+        const int e = i < n ? a.idx[i] : -1;
+        const bool ok = e >= 0 && e < a.E;
+        const uint64_t wrong = __ballot(!ok && e != -1);
+        uint64_t same = __ballot(ok);
+        for (int b = 0; (a.E - 1) >> b; ++b) {
+            const uint64_t set = __ballot(e >> b & 1);
+            same &= e >> b & 1 ? set : ~set;
+        }
+        const uint64_t below = (uint64_t{1} << i) - 1, token = below & ~((uint64_t{1} << (i - i % a.K)) - 1);
+        // an entry whose expert the token names before it is left out
+        const bool keep = ok && !(same & token);
+        const uint64_t kept = __ballot(keep);
+        same &= kept;
+        const int m = __popcll(same), rank = __popcll(same & below);
+        const bool leads = keep && rank == 0;
+        int i0 = 0, b0 = 0, f0 = 0, all = 0;  // experts, entries and tiles before this one's, and all tiles
+        const uint64_t leaders = __ballot(leads);
+        for (uint64_t left = leaders; left; left &= left - 1) {
+            const int j = __ffsll(static_cast<unsigned long long>(left)) - 1;
+            const int ej = __builtin_amdgcn_readlane(e, j), mj = __builtin_amdgcn_readlane(m, j);
+            const int tj = (mj + width - 1) / width;
+            if (ej < e) ++i0, b0 += mj, f0 += tj;
+            all += tj;
+        }
+        if (i < n) id[i] = static_cast<int16_t>(ok ? e : -1);
+        if (keep) entry[b0 + rank] = static_cast<uint16_t>(i);
+        if (leads) {
+            expert[i0] = static_cast<uint16_t>(e);
+            begin[i0] = b0;
+            first[i0] = f0;
+            for (int t = 0; t * width < m; ++t) owner[f0 + t] = static_cast<uint16_t>(i0);
+        }
+        if (i == 0) {
+            experts = __popcll(leaders);
+            begin[experts] = __popcll(kept);
+            first[experts] = all;
+            bad = wrong != 0;
+        }
     }
 };
 
@@ -363,9 +420,7 @@ __global__ __launch_bounds__(kFewThreads, 2) void tokens_up_fp4_kernel(TokensArg
     __shared__ Part<2> part;
     extern __shared__ __attribute__((aligned(16))) char dynamic[];
     Lists l(a, dynamic);
-    sort_entries(a, l);
-    l.order<kFewThreads>();
-    l.tiles<kFewThreads>(XC);
+    l.fill<kFewThreads, true>(a, XC);
     if (blockIdx.x == 0 && threadIdx.x == 0) *a.status = l.bad ? EP_ERR_BAD_EXPERT : EP_OK;
     const Lanes ll;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -378,12 +433,12 @@ __global__ __launch_bounds__(kFewThreads, 2) void tokens_up_fp4_kernel(TokensArg
         clear(acc);
         int e = 0, n0 = 0, c0 = 0, s0 = 0, m = 0;
         if (item < items) {
-            const int i = tile_expert(l.first, experts, item / nf);
+            const int i = __builtin_amdgcn_readfirstlane(l.owner[item / nf]);
             const int f0 = __builtin_amdgcn_readfirstlane(l.first[i]), nt = __builtin_amdgcn_readfirstlane(l.first[i + 1]) - f0;
             int tt, ft;
             tile_in_expert(item - f0 * nf, nt, nf, &tt, &ft);
             e = __builtin_amdgcn_readfirstlane(l.expert[i]);
-            s0 = __builtin_amdgcn_readfirstlane(l.start(e)), m = __builtin_amdgcn_readfirstlane(l.end[e]) - s0;
+            s0 = __builtin_amdgcn_readfirstlane(l.begin[i]), m = __builtin_amdgcn_readfirstlane(l.begin[i + 1]) - s0;
             n0 = ft * kOut, c0 = tt * XC;
             Rows<2, XC> r;
             set_weights(r, a.w1, a.w1_sf, e, a.M, a.H, {n0, GATED ? a.I + n0 : n0 + 16}, ll);
@@ -401,51 +456,49 @@ __global__ __launch_bounds__(kFewThreads, 2) void tokens_up_fp4_kernel(TokensArg
     }
 }
 
-// down: one workgroup for each 16 FF outputs, all experts, each wave whole
-// tiles of entries in turn, or shares of their k where there are fewer tiles than
-// waves; the sums of every token are each wave's own in LDS, joined at the end.
-template <int FF, int NT, int XC>
+// down: one workgroup for each 16 outputs, all experts, each wave whole tiles
+// of entries in turn, or shares of their k where there are fewer tiles than waves;
+// the sums of every token are each wave's own in LDS, joined at the end.  (One
+// stream of stages through all of a wave's tiles, with its loads ahead across the
+// tiles' ends, takes more instructions a stage: 128 tokens of 256 experts 1340
+// us, 1270 without.)
+template <int NT, int XC>
 __global__ __launch_bounds__(NT, 2) void tokens_down_fp4_kernel(TokensArgs a) {
     constexpr int kWaves = NT / 64;
-    __shared__ __attribute__((aligned(16))) char scratch[kWaves][kScratch<FF, XC>];
+    __shared__ __attribute__((aligned(16))) char scratch[kWaves][kScratch<1, XC>];
     extern __shared__ __attribute__((aligned(16))) char dynamic[];
     Lists l(a, dynamic);
     float *sums = reinterpret_cast<float *>(dynamic + Lists::bytes(a));
-    sort_entries<NT>(a, l);
-    l.tiles<NT>(XC);
+    l.fill<NT, false>(a, XC);  // a workgroup's own
     const Lanes ll;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int n0 = blockIdx.x * 16 * FF;
-    const int size = a.T * 16 * FF;  // floats of a wave's sums
+    const int n0 = blockIdx.x * 16;
+    const int size = a.T * 16;  // floats of a wave's sums
     float *mine = sums + wave * size;
     for (int i = __lane_id() * 4; i < size; i += 256) *reinterpret_cast<f32x4 *>(mine + i) = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    const int experts = __builtin_amdgcn_readfirstlane(l.experts), tiles = __builtin_amdgcn_readfirstlane(l.first[experts]);
+    const int tiles = __builtin_amdgcn_readfirstlane(l.first[__builtin_amdgcn_readfirstlane(l.experts)]);
     const int shares = tiles >= kWaves ? 1 : tiles ? kWaves / tiles : 1;
     for (int u = wave; u < tiles * shares; u += kWaves) {
-        const int i = tile_expert(l.first, experts, u / shares);
+        const int t = u / shares, i = __builtin_amdgcn_readfirstlane(l.owner[t]);
         const int e = __builtin_amdgcn_readfirstlane(l.expert[i]);
-        const int c0 = (u / shares - __builtin_amdgcn_readfirstlane(l.first[i])) * XC;
-        const int s0 = __builtin_amdgcn_readfirstlane(l.start(e)), m = __builtin_amdgcn_readfirstlane(l.end[e]) - s0;
-        Rows<FF, XC> r;
-        int row[FF];
-#pragma unroll
-        for (int f = 0; f < FF; ++f) row[f] = n0 + f * 16;
-        set_weights(r, a.w2, a.w2_sf, e, a.H, a.I, row, ll);
+        const int c0 = (t - __builtin_amdgcn_readfirstlane(l.first[i])) * XC;
+        const int s0 = __builtin_amdgcn_readfirstlane(l.begin[i]), m = __builtin_amdgcn_readfirstlane(l.begin[i + 1]) - s0;
+        Rows<1, XC> r;
+        set_weights(r, a.w2, a.w2_sf, e, a.H, a.I, {n0}, ll);
         r.x = reinterpret_cast<const char *>(a.h);
 #pragma unroll
         for (int h = 0; h < XC / 8; ++h)
             r.x_at[h] = static_cast<uint32_t>(l.entry[s0 + min(c0 + h * 8 + ll.row, m - 1)]) * a.I * 2 + (ll.piece ^ h) * 16;
-        f32x4 acc[FF];
+        f32x4 acc[1];
         clear(acc);
-        accumulate<2>(acc, r, a.I, u % shares, shares, scratch[wave], ll);
+        accumulate<2>(acc, r, a.I, u - t * shares, shares, scratch[wave], ll);
         if (c0 + ll.li < m && ll.li < XC) {
             const int tok = l.entry[s0 + c0 + ll.li] / a.K;
-#pragma unroll
-            for (int f = 0; f < FF; ++f) *reinterpret_cast<f32x4 *>(mine + tok * (16 * FF) + f * 16 + ll.lg * 4) += acc[f];
+            *reinterpret_cast<f32x4 *>(mine + tok * 16 + ll.lg * 4) += acc[0];
         }
     }
     __syncthreads();
-    down_write<FF, NT>(a, l, sums, n0);
+    down_write<1, NT>(a, l, sums, n0);
 }
 
 constexpr int kFp4Workgroups = 256;  // one a CU, which its registers fill
@@ -475,19 +528,19 @@ hipError_t launch_up(const TokensArgs &a, hipStream_t stream) {
     return hipGetLastError();
 }
 
-template <int FF, int NT, int XC>
+template <int NT, int XC>
 hipError_t launch_down(const TokensArgs &a, hipStream_t stream) {
-    const int lds = Lists::bytes(a) + NT / 64 * a.T * 16 * FF * 4;
-    tokens_down_fp4_kernel<FF, NT, XC><<<a.H / (16 * FF), NT, lds, stream>>>(a);
+    tokens_down_fp4_kernel<NT, XC><<<a.H / 16, NT, Lists::bytes(a) + NT / 64 * a.T * 16 * 4, stream>>>(a);
     return hipGetLastError();
 }
 
-// 32 outputs a workgroup where the tokens' sums leave a CU's LDS to one workgroup anyway; four waves a workgroup where
-// there are more workgroups than CUs.
+// Eight waves a workgroup, or four where there are more workgroups than CUs, so that two fit one: one token of 7168
+// channels and 8 experts 55.9 and 50.4 us, 9 tokens of 3424 channels 43.0 and 47.5.  32 outputs a workgroup were no faster
+// with 128 tokens (1275 and 1278 us).
 template <int XC>
 hipError_t launch_down_rows(const TokensArgs &a, hipStream_t stream) {
-    if (a.H <= 16 * kFp4Workgroups) return launch_down<1, 512, XC>(a, stream);
-    return a.T > 16 ? launch_down<2, 256, XC>(a, stream) : launch_down<1, 256, XC>(a, stream);
+    const bool fits = Lists::bytes(a) + kFewWaves * (kScratch<1, XC> + a.T * 16 * 4) <= 160 * 1024;  // a CU's LDS
+    return a.H > 16 * kFp4Workgroups || !fits ? launch_down<256, XC>(a, stream) : launch_down<512, XC>(a, stream);
 }
 
 }  // namespace
