@@ -49,7 +49,7 @@ int statistics(const ep_problem *p, int32_t *expert_count, int32_t *token_count,
                void *workspace, size_t workspace_bytes, epget::RouteArgs *a) {
     if (!expert_count || !token_count || !prob_sum || !losses || !workspace) return EP_ERR_INVALID_ARG;
     if (!aligned4(expert_count, token_count, prob_sum, losses) || !aligned(workspace, 256)) return EP_ERR_INVALID_ARG;
-    if (workspace_bytes < static_cast<size_t>(epget::route_workspace(p->num_tokens, p->num_experts)))
+    if (workspace_bytes < static_cast<size_t>(epget::route_workspace(p->num_tokens, p->num_experts, p->num_topk)))
         return EP_ERR_INVALID_ARG;
     a->expert_count = expert_count;
     a->token_count = token_count;
@@ -78,7 +78,7 @@ extern "C" {
 
 size_t ep_route_workspace_bytes(const ep_problem *p, const ep_router *r) {
     if (check_router(p, r) != EP_OK) return 0;
-    return static_cast<size_t>(epget::route_workspace(p->num_tokens, p->num_experts));
+    return static_cast<size_t>(epget::route_workspace(p->num_tokens, p->num_experts, p->num_topk));
 }
 
 int ep_route(const ep_problem *p, const ep_router *r, const void *logits, const float *bias, const uint8_t *token_mask,

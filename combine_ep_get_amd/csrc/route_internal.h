@@ -26,10 +26,8 @@ struct RouteArgs {
     void *dlogits;
 };
 
-// Workgroups of a call that gathers statistics, and bytes of the partial sums
-// that they leave.
-int32_t route_stat_workgroups(int32_t T, int32_t E);
-int64_t route_workspace(int32_t T, int32_t E);
+// Bytes of the partial sums that a call with statistics leaves.
+int64_t route_workspace(int32_t T, int32_t E, int32_t K);
 
 hipError_t launch_route(const RouteArgs &a, hipStream_t stream);
 hipError_t launch_balance(const RouteArgs &a, hipStream_t stream);

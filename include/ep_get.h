@@ -184,7 +184,7 @@ size_t ep_route_workspace_bytes(const ep_problem *problem, const ep_router *rout
  *   logits       [T,E] fp32 or bf16 device (router->logits_bf16), 16-byte aligned
  *   bias         [E] fp32 device, or NULL; in the choice only
  *   token_mask   [T] uint8 device, or NULL; 0 marks a token that is padding:
- *                its logits are not read, its entries are -1 with weight 0
+ *                its logits do not matter, its entries are -1 with weight 0
  *   topk_idx     [T,K] int32 device, written
  *   topk_weights [T,K] fp32 device, written
  * and, for training, the statistics of the V tokens that count (those that
