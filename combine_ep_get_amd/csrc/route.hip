@@ -196,7 +196,7 @@ struct Columns {
 // exp(x) for x <= 0 or NaN, within two ulp: the hardware's exp2 of the rounded
 // product, corrected by what the rounding dropped.
 __device__ __forceinline__ float exp_down(float x) {
-    const float c = x < -200.0f ? -200.0f : x;  // -inf has no product's remainder; NaN stays
+    const float c = __builtin_elementwise_maximum(x, -200.0f);  // -inf has no product's remainder; NaN stays
     const float t = c * 1.4426950408889634f;
     const float lo = __builtin_fmaf(c, 1.9259629911266175e-8f, __builtin_fmaf(c, 1.4426950408889634f, -t));
     const float r = __builtin_amdgcn_exp2f(t);
@@ -209,7 +209,7 @@ __device__ __forceinline__ float logistic(float x) { return 1.0f / (1.0f + expf(
 __device__ __forceinline__ float quick_logistic(float x, float *rcp) {
     const float t = exp_down(-fabsf(x));
     *rcp = __builtin_amdgcn_rcpf(1.0f + t);
-    return (x >= 0.0f ? 1.0f : x < 0.0f ? t : x) * *rcp;
+    return (x >= 0.0f ? 1.0f : t) * *rcp;  // NaN by the reciprocal
 }
 
 // sigmoid(x) exp(-c) with c = min(top, 0), which no row of small logits takes to 0: e = exp(x - top).
@@ -296,8 +296,9 @@ __device__ __forceinline__ void write_losses(const RouteArgs &a, double balance,
 template <int L, int N>
 constexpr int kColumnBits = __builtin_ctz(L * N);
 
+// Rises with v, which is no -0.
 __device__ __forceinline__ uint32_t ordered_bits(float v) {
-    const uint32_t u = __float_as_uint(v + 0.0f);  // -0 is 0
+    const uint32_t u = __float_as_uint(v);
     return u ^ (static_cast<uint32_t>(static_cast<int32_t>(u) >> 31) | 0x80000000u);
 }
 __device__ __forceinline__ float ordered_value(uint32_t k) {
@@ -470,21 +471,27 @@ __global__ __launch_bounds__((kThreads<MODE, L, N>)) void route_kernel(RouteArgs
         Softmax r = {};
         if (STATS || (!sigmoid && (biased || !a.normalise))) r = softmax<L>(x, e);
         // keys, and of e the numerators of the probabilities
+        const float *my_bias = bias + l * C::V;
+        const uint32_t my_low = kLow - l * C::V;
+        auto key_of = [&](float v, int i) { return (ordered_bits(v) & ~kLow) | (my_low - C::at(i)); };
         float all = 0.0f;
+        if (sigmoid && (STATS || biased)) {
+            const bool low = r.top < 0.0f;
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            float v = x[i];
-            if (sigmoid && (STATS || biased)) {
+            for (int i = 0; i < N; ++i) {
                 float rcp;
                 const float s = quick_logistic(x[i], &rcp);
-                if (STATS) e[i] = r.top < 0.0f ? e[i] * rcp : s, all += e[i];
-                if (biased) v = s + bias[l * C::V + C::at(i)];
-            } else if (biased) {
-                v = e[i] * r.rcp + bias[l * C::V + C::at(i)];
+                if (STATS) e[i] = low ? e[i] * rcp : s, all += e[i];
+                if (CHOOSE) {
+                    const float v = x[i] > -INFINITY ? (biased ? s + my_bias[C::at(i)] : x[i] + 0.0f) : -INFINITY;
+                    key[i] = v > -INFINITY ? key_of(v, i) : 0;
+                }
             }
-            if (CHOOSE) {
-                const uint32_t k = (ordered_bits(v) & ~kLow) | (kLow - (l * C::V + C::at(i)));
-                key[i] = x[i] > -INFINITY && v > -INFINITY ? k : 0;
+        } else if (CHOOSE) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const float v = x[i] > -INFINITY ? (biased ? __builtin_fmaf(e[i], r.rcp, my_bias[C::at(i)]) : x[i] + 0.0f) : -INFINITY;
+                key[i] = v > -INFINITY ? key_of(v, i) : 0;
             }
         }
         if (STATS) {
