@@ -22,7 +22,7 @@ constexpr int kTableSize = 64;
 constexpr int kGradThreads = 256;
 constexpr int kVectors = 8;                                 // 16-byte vectors of a thread and piece
 constexpr int kPiece = kGradThreads * kVectors * 16;        // bytes
-constexpr int kGradWorkgroups = 2048;
+constexpr int kGradWorkgroups = 4096;
 
 struct GradTable {
     const char *grad[kTableSize];
