@@ -147,6 +147,8 @@ class Grads:
         outs = grads if outs is None else list(outs)
         if len(outs) != len(grads):
             raise ValueError(f"outs: {len(outs)} tensors for {len(grads)} gradients")
+        if len({t.device for t in (*grads, *outs)}) > 1:
+            raise ValueError("gradients on more than one device: a list, and a sum, for each")
         types = {torch.bfloat16: (EP_GRAD_BF16, "bf16"), torch.float32: (EP_GRAD_FP32, "float")}
         array = (Grad * len(grads))()
         for i, (g, o) in enumerate(zip(grads, outs)):
@@ -333,6 +335,18 @@ def _stream(stream):
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
+
+
+def _on_current_device(stream, *tensors) -> None:
+    """The calls run on the current device, unless the caller names a stream: refuses tensors of another one."""
+    if stream is not None:
+        return
+    import torch
+    here = torch.cuda.current_device() if any(t is not None and not isinstance(t, int) for t in tensors) else -1
+    for t in tensors:
+        if t is not None and not isinstance(t, int) and t.get_device() != here:
+            raise ValueError(f"a tensor on device {t.get_device()} with device {here} current; "
+                             "use torch.cuda.device(...) around the call")
 
 
 def error_string(code: int) -> str:
@@ -644,6 +658,7 @@ def ep_expert_product_fp4(problem, product, x, expert_count, expert_offset, w_fp
     """ep_expert_product of up to EP_MOE_TOKENS_MAX tokens with MXFP4 weights:
     e2m1 codes, two a byte, and one e8m0 scale for each 32 of a row."""
     E, C, N, M, rows = _product_sizes(problem, product, expert_count)
+    _on_current_device(stream, x, w_fp4, w_sf, out)
     return _run("ep_expert_product_fp4", problem, (_product_ref(product, bind), _arg(x, "x", "bf16", rows * C),
         _arg(expert_count, "expert_count", "int32", E), _arg(expert_offset, "expert_offset", "int32", E),
         _arg(w_fp4, "w_fp4", "e2m1", E * M * C // 2), _arg(w_sf, "w_sf", "e8m0", E * M * (C // 32)),
@@ -654,6 +669,7 @@ def ep_expert_product_fp4(problem, product, x, expert_count, expert_offset, w_fp
 def ep_moe_tokens_fp4(problem, product, x, topk_idx, topk_weights, w1_fp4, w1_sf, b1, w2_fp4, w2_sf, b2, residual, out,
                       workspace, workspace_bytes=None, stream=None, bind=False):
     """ep_moe_tokens with MXFP4 weights."""
+    _on_current_device(stream, x, w1_fp4, w2_fp4, out, workspace)
     return _run("ep_moe_tokens_fp4", problem, _tokens_ptrs(problem, product, x, topk_idx, topk_weights, w1_fp4, w1_sf,
         b1, w2_fp4, w2_sf, b2, residual, out, workspace, workspace_bytes, "e2m1", stream, bind), bind)
 
@@ -680,6 +696,7 @@ def ep_route(problem, router, logits, bias, token_mask, topk_idx, topk_weights, 
     """The router: top-k experts and their weights from the logits, and with
     the last arguments the counts, the balance loss and the z loss."""
     T, _, K, E, _, _, _ = _sizes(problem)
+    _on_current_device(stream, logits, topk_idx, topk_weights, workspace)
     return _run("ep_route", problem, (_product_ref(router, bind), _arg(logits, "logits", _logits_type(router), T * E),
         _arg(bias, "bias", "float", E), _arg(token_mask, "token_mask", "uint8", T),
         _arg(topk_idx, "topk_idx", "int32", T * K), _arg(topk_weights, "topk_weights", "float", T * K),
@@ -691,6 +708,7 @@ def ep_balance_loss(problem, router, logits, topk_idx, token_mask, expert_count,
                     workspace, workspace_bytes=None, stream=None, bind=False):
     """The counts, the balance loss and the z loss of choices made elsewhere."""
     T, _, K, E, _, _, _ = _sizes(problem)
+    _on_current_device(stream, logits, topk_idx, workspace)
     return _run("ep_balance_loss", problem, (_product_ref(router, bind),
         _arg(logits, "logits", _logits_type(router), T * E), _arg(topk_idx, "topk_idx", "int32", T * K),
         _arg(token_mask, "token_mask", "uint8", T),
@@ -703,6 +721,7 @@ def ep_route_backward(problem, router, logits, topk_idx, token_mask, expert_coun
     """The logits' gradient from those of the weights (None: without) and of
     the two losses (None: without)."""
     T, _, K, E, _, _, _ = _sizes(problem)
+    _on_current_device(stream, logits, dweights, dlogits)
     return _run("ep_route_backward", problem, (_product_ref(router, bind),
         _arg(logits, "logits", _logits_type(router), T * E), _arg(topk_idx, "topk_idx", "int32", T * K),
         _arg(token_mask, "token_mask", "uint8", T), _arg(expert_count, "expert_count", "int32", E),
@@ -736,12 +755,14 @@ def ep_grad_square_sum(grads, square_sum, workspace, workspace_bytes=None, strea
     ranks with gradients of their own add theirs up before ep_grad_clip."""
     if workspace_bytes is None:
         workspace_bytes = workspace.numel() * workspace.element_size()
+    _on_current_device(stream, square_sum, workspace, *grads.tensors[0][:1])
     return _run_grads("ep_grad_square_sum", grads, (_arg(square_sum, "square_sum", "double", 1),
         _arg(workspace, "workspace", "bytes", workspace_bytes), workspace_bytes, _stream(stream)), bind)
 
 
 def ep_grad_clip(grads, square_sum, max_norm, norm=None, stream=None, bind=False):
     """out = grad * min(1, max_norm / sqrt(square_sum)), and the norm."""
+    _on_current_device(stream, square_sum, norm, *grads.tensors[0][:1])
     return _run_grads("ep_grad_clip", grads, (_arg(square_sum, "square_sum", "double", 1), max_norm,
         _arg(norm, "norm", "float", 1), _stream(stream)), bind)
 

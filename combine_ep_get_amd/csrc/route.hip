@@ -650,7 +650,7 @@ __global__ __launch_bounds__(kRouteThreads) void route_backward_kernel(RouteArgs
         float c = 0.0f, sum = 0.0f;
         if (a.dw) {
             C::keep(x, row);
-            if (!(on && l < a.K && pick >= 0 && pick < a.E)) pick = -1;
+            if (!(on && l < a.K && pick >= 0 && pick < a.E)) pick = -1, g = 0.0f;  // whatever dweights hold there
             const float val = pick >= 0 ? row[C::place(pick)] : -INFINITY;
             if (a.normalise) {
                 const float top = group_max<L>(val);

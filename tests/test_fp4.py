@@ -117,6 +117,9 @@ TOKENS = [
     (128, 64, 32, 300, 32, "geglu", True, True, True, True, 0.1),
     (100, 4128, 32, 2, 2, "silu", False, False, True, False, 0.0),   # 32 outputs a workgroup of the down product
     (2, 1056, 1312, 8, 8, "swiglu", False, True, True, False, 0.0),
+    (2, 64, 32, 9, 32, "silu", True, True, True, True, 0.3),           # 64 entries: one wave sorts them
+    (128, 32, 32, 2048, 32, "relu", True, False, True, False, 0.0),    # the most experts and entries
+    (1, 7168, 64, 3, 2, "gelu", False, True, False, False, 0.0),       # more workgroups than CUs
 ]
 
 
@@ -125,7 +128,9 @@ def test_tokens(ep, case):  # noqa: F811
     T, H, I, E, K, act, bias, residual, weights, twice, empty = case
     g = torch.Generator().manual_seed(T)
     idx = route(g, T, E, K, empty, twice)
-    p, q = problem(ep, T, H, E, K), ep.Product.make(H, I, ref.ACTS.index(act))
+    p, q = ep.Problem.make(T, H, E, K, max(1, E // 150), 1, 1, 1), ep.Product.make(H, I, ref.ACTS.index(act))
+    while E % p.num_ranks:
+        p.num_ranks += 1
     M = q.weight_rows
     x, (w1, s1), (w2, s2) = normal(g, T, H), weight(g, E, M, H), weight(g, E, H, I)
     b1, b2 = (torch.randn(E, M, generator=g), torch.randn(E, H, generator=g)) if bias else (None, None)

@@ -402,3 +402,54 @@ def test_many_tokens(ep):  # noqa: F811
     value, bound = ref.gradient(0, True, 1.0, logits, want, mask, st["expert_count"][0], st["token_count"][0], None,
                                 torch.tensor([1e4, 1.0]), K, True)
     assert_within(got, value, bound)
+
+
+@pytest.mark.parametrize("E,K", [(20, 4), (100, 8), (256, 12), (256, 13)])
+def test_many_tokens_whose_order_is_close(ep, E, K):  # noqa: F811
+    """As the equal logits and the close sums above, with four tokens a wave: rows of equal values, of few values, and of
+    sums that only 64 bits tell apart, among ordinary ones."""
+    T = 1500
+    g = torch.Generator().manual_seed(E + K)
+    logits = torch.randn(T, E, generator=g)
+    logits[100:300] = 0.25
+    logits[300:500] = torch.randint(-1, 2, (200, E), generator=g).float()
+    for kind in (0, 1):
+        s = ref.scores(kind, logits[1000:1001].double())[0][0]
+        for bias in (None, torch.zeros(E), (0.75 - s).float()):
+            x = logits.clone()
+            x[1000:1200:3] = logits[1000]
+            c = Call(ep, x, K, kind, bias=bias)
+            c.check_choices(*c.route(stats=True))
+        c = Call(ep, logits.bfloat16(), K, kind)
+        c.check_choices(*c.route())
+
+
+def test_gradients_of_weights_that_are_not_there(ep):  # noqa: F811
+    """What dweights hold for empty entries and padded tokens does not matter."""
+    for T in (30, 1100):
+        E, K = 24, 4
+        logits, mask, g = inputs(T, E, False, 21, 0.2)
+        idx = ref.choose(0, logits, None, mask, K)
+        idx[3, 2] = -1
+        idx[4] = -1
+        dw = torch.randn(T, K, generator=g)
+        for kind in (0, 1):
+            for normalise in (True, False):
+                c = Call(ep, logits, K, kind, normalise, mask=mask)
+                want = c.backward(idx, None, None, dw, None)
+                worse = dw.clone()
+                worse[3, 2] = NAN
+                worse[4] = INF
+                worse[mask == 0] = NAN
+                assert torch.equal(c.backward(idx, None, None, worse, None), want)
+                assert not want[4].any() and not want[mask == 0].any()
+
+
+def test_another_device_is_refused(ep, monkeypatch):  # noqa: F811
+    logits, _, _ = inputs(4, 8, False, 1)
+    c = Call(ep, logits, 2)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    with pytest.raises(ValueError, match="device 0 with device 1 current"):
+        c.route()
+    with pytest.raises(ValueError, match="device 0 with device 1 current"):
+        ep.ep_grad_clip(ep.Grads.make([torch.ones(3, device="cuda")]), torch.ones(1, dtype=torch.float64, device="cuda"), 1.0)
