@@ -8,7 +8,11 @@
 // whichever gradient they belong to, so many small gradients and a few
 // large ones fill the chip alike.  Squares are summed in 64 bits: an fp32
 // square of a large gradient overflows, and the sum of 10^9 small ones loses
-// its last digits.  Both calls are bound by memory.
+// its last digits.
+//
+// Both calls are bound by memory.  2.8 GB of gradients: the sum 480 us (5.9 TB/s), the clipping 1030 us, a read and a write
+// at 5.5 TB/s; together 1515 us with 4096 workgroups, 1538 with 2048.  The clipping's loads and stores are past the caches:
+// 1610 us with ordinary ones.  40 small gradients: 5, 2 and 7 us, launches for the most part.
 #include "../../include/ep_get.h"
 #include "device_common.h"
 #include "grads_internal.h"
@@ -50,11 +54,15 @@ __device__ __forceinline__ float element(const char *p, int64_t i, bool fp32) {
     return fp32 ? reinterpret_cast<const float *>(p)[i] : bf16_lo(reinterpret_cast<const uint16_t *>(p)[i]);
 }
 
-__device__ __forceinline__ void put(char *p, int64_t i, bool fp32, float v) {
-    if (fp32)
-        reinterpret_cast<float *>(p)[i] = v;
-    else
-        reinterpret_cast<uint16_t *>(p)[i] = __builtin_bit_cast(uint16_t, static_cast<__bf16>(v));
+// out[i] = p[i] * f, or its very bits without `scale`
+__device__ __forceinline__ void move(char *out, const char *p, int64_t i, bool fp32, bool scale, float f) {
+    if (fp32) {
+        const uint32_t v = reinterpret_cast<const uint32_t *>(p)[i];
+        reinterpret_cast<uint32_t *>(out)[i] = scale ? __float_as_uint(__uint_as_float(v) * f) : v;
+    } else {
+        const uint16_t v = reinterpret_cast<const uint16_t *>(p)[i];
+        reinterpret_cast<uint16_t *>(out)[i] = scale ? __builtin_bit_cast(uint16_t, static_cast<__bf16>(bf16_lo(v) * f)) : v;
+    }
 }
 
 __device__ __forceinline__ double square(float v) { return static_cast<double>(v) * v; }
@@ -161,15 +169,7 @@ __global__ __launch_bounds__(kGradThreads) void clip_kernel(GradTable t, const d
         Span s = span_of(p, t.count[g], piece - t.first[g], size);
         if ((reinterpret_cast<uintptr_t>(p) ^ reinterpret_cast<uintptr_t>(out)) & 15) {
             // no 16-byte vector is aligned on both sides
-            for (int64_t i = s.begin + threadIdx.x; i < s.end; i += kGradThreads) {
-                if (scale) {
-                    put(out, i, fp32, element(p, i, fp32) * f);
-                } else if (fp32) {
-                    reinterpret_cast<uint32_t *>(out)[i] = reinterpret_cast<const uint32_t *>(p)[i];
-                } else {
-                    reinterpret_cast<uint16_t *>(out)[i] = reinterpret_cast<const uint16_t *>(p)[i];
-                }
-            }
+            for (int64_t i = s.begin + threadIdx.x; i < s.end; i += kGradThreads) move(out, p, i, fp32, scale, f);
             continue;
         }
         const u32x4 *v = reinterpret_cast<const u32x4 *>(p + s.vec * size);
@@ -187,8 +187,8 @@ __global__ __launch_bounds__(kGradThreads) void clip_kernel(GradTable t, const d
             if (at < n) __builtin_nontemporal_store(scale ? scaled(d[i], fp32, f) : d[i], o + at);
         }
         const int64_t head = s.begin + threadIdx.x, tail = s.vec_end + threadIdx.x;
-        if (head < s.vec) put(out, head, fp32, element(p, head, fp32) * f);
-        if (tail < s.end) put(out, tail, fp32, element(p, tail, fp32) * f);
+        if (head < s.vec) move(out, p, head, fp32, scale, f);
+        if (tail < s.end) move(out, p, tail, fp32, scale, f);
     }
 }
 

@@ -135,6 +135,19 @@ def test_norms_that_are_not_finite_scale_nothing(ep):  # noqa: F811
             assert torch.equal(o.nan_to_num(1e9, 2e9, 3e9), b.nan_to_num(1e9, 2e9, 3e9))
 
 
+@pytest.mark.parametrize("shift", [0, 1])
+def test_unscaled_gradients_keep_their_bits(ep, shift):  # noqa: F811
+    """Signalling NaNs too, in whole vectors and in what lies before and after them."""
+    for dtype, bits, pattern in ((FP, torch.int32, 0x7F800001), (BF, torch.int16, 0x7F81)):
+        buf = torch.randn(5010, device="cuda").to(dtype)
+        for at in (0, 1, 6, 7, 100, 4997, 4998, 4999):
+            buf.view(bits)[1 + at] = pattern
+        grad = buf[1:5001]
+        out = torch.zeros(5010, device="cuda", dtype=dtype)[1 + shift:5001 + shift]
+        norm, _ = clip(ep, [grad], [out], 0.1)
+        assert math.isnan(norm) and torch.equal(out.view(bits), grad.view(bits))
+
+
 def test_no_gradients(ep):  # noqa: F811
     assert clip(ep, [], [], 1.0) == (0.0, 0.0)
     empty = torch.empty(0, device="cuda")
