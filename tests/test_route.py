@@ -178,6 +178,20 @@ def test_equal_logits_go_to_the_lowest_expert(ep):  # noqa: F811
                     c.check_choices(*c.route())
 
 
+@pytest.mark.parametrize("E", [128, 129])
+@pytest.mark.parametrize("T", [16, 32, 33, 64, 1024, 1025, 4096, 4097])
+def test_where_forms_change(ep, T, E):  # noqa: F811
+    """Both sides of the numbers of tokens at which another number of workgroups or of lanes works."""
+    logits, _, g = inputs(T, E, T % 2 == 1, T, 0.0)
+    c = Call(ep, logits, 6, 1, True, 1.0, torch.randn(E, generator=g) * 0.2)
+    want = c.check_choices(*c.route(stats=True))
+    c.check_stats(want)
+    first = [t.clone() for t in c.stats]
+    c.fresh()
+    c.balance(want)
+    assert all(torch.equal(a[:-1], b[:-1]) for a, b in zip(first, c.stats))
+
+
 def test_signed_zeros_are_equal(ep):  # noqa: F811
     logits = torch.tensor([[0.0, -0.0, 0.0, -0.0, -1.0], [-0.0, 0.0, -0.0, 0.0, 1.0]])
     idx, _ = Call(ep, logits, 4).route()
