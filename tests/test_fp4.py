@@ -115,11 +115,12 @@ TOKENS = [
     (90, 352, 96, 64, 8, "swiglu", True, True, True, False, 0.1),
     (128, 64, 64, 2, 2, "swiglu", False, True, True, False, 0.0),
     (128, 64, 32, 300, 32, "geglu", True, True, True, True, 0.1),
-    (100, 4128, 32, 2, 2, "silu", False, False, True, False, 0.0),   # 32 outputs a workgroup of the down product
+    (100, 4128, 32, 2, 2, "silu", False, False, True, False, 0.0),   # the down product in workgroups of four waves
     (2, 1056, 1312, 8, 8, "swiglu", False, True, True, False, 0.0),
     (2, 64, 32, 9, 32, "silu", True, True, True, True, 0.3),           # 64 entries: one wave sorts them
     (128, 32, 32, 2048, 32, "relu", True, False, True, False, 0.0),    # the most experts and entries
     (1, 7168, 64, 3, 2, "gelu", False, True, False, False, 0.0),       # more workgroups than CUs
+    (28, 64, 96, 8, 2, "swiglu", False, False, True, False, 0.0),      # the fewest entries an expert for tiles of sixteen
 ]
 
 
