@@ -152,12 +152,20 @@ template <int DEPTH, int FF, int XC>
 __device__ __forceinline__ void accumulate(f32x4 (&acc)[FF], const Rows<FF, XC> &r, int K, int first, int step,
                                            char *scratch, const Lanes &ll) {
     const int full = K / kStageK;
-    const int n = first < full ? (full - first + step - 1) / step : 0;
+    const int n = first < full ? (full - first + step - 1) / step : 0;  // whole stages
+    const bool rest = K % kStageK && full % step == first;              // and stage n, in part past K
     Stage<FF, XC> s[DEPTH];
+    auto load = [&](int i, int at) {
+        if (at < n)
+            load_stage<true>(s[i], r, first + at * step, K, ll);
+        else if (at == n && rest)
+            load_stage<false>(s[i], r, full, K, ll);
+    };
+    const int all = n + rest;
+    int at = 0;  // the stage in s[0]
     if (n >= DEPTH) {
 #pragma unroll
         for (int i = 0; i < DEPTH; ++i) load_stage<true>(s[i], r, first + i * step, K, ll);
-        int at = 0;  // the stage in s[0]
         for (; at + 2 * DEPTH <= n; at += DEPTH) {
 #pragma unroll
             for (int i = 0; i < DEPTH; ++i) {
@@ -165,27 +173,20 @@ __device__ __forceinline__ void accumulate(f32x4 (&acc)[FF], const Rows<FF, XC> 
                 load_stage<true>(s[i], r, first + (at + i + DEPTH) * step, K, ll);
             }
         }
-        // fewer than 2 DEPTH are left
+        // fewer than 2 DEPTH whole ones are left
 #pragma unroll
         for (int i = 0; i < DEPTH; ++i) {
             use_stage(acc, s[i], scratch, ll);
-            if (at + i + DEPTH < n) load_stage<true>(s[i], r, first + (at + i + DEPTH) * step, K, ll);
+            load(i, at + i + DEPTH);
         }
-#pragma unroll
-        for (int i = 0; i < DEPTH - 1; ++i)
-            if (at + i + DEPTH < n) use_stage(acc, s[i], scratch, ll);
+        at += DEPTH;
     } else {
 #pragma unroll
-        for (int i = 0; i < DEPTH - 1; ++i)
-            if (i < n) load_stage<true>(s[i], r, first + i * step, K, ll);
+        for (int i = 0; i < DEPTH; ++i) load(i, i);
+    }
 #pragma unroll
-        for (int i = 0; i < DEPTH - 1; ++i)
-            if (i < n) use_stage(acc, s[i], scratch, ll);
-    }
-    if (K % kStageK && full % step == first) {
-        load_stage<false>(s[0], r, full, K, ll);
-        use_stage(acc, s[0], scratch, ll);
-    }
+    for (int i = 0; i < DEPTH; ++i)
+        if (at + i < all) use_stage(acc, s[i], scratch, ll);
 }
 
 template <int FF>
@@ -310,24 +311,26 @@ __global__ __launch_bounds__(kFewThreads, 2) void product_fp4_kernel(ProductArgs
 
 // The entries by expert and their tiles, in LDS that the launch sizes.
 struct Lists {
-    int *end;                  // sort_entries' (by expert)
-    int *begin, *first;        // entries and tiles of the experts (with entries) before each
-    int *wave_sum;
-    uint16_t *expert, *entry;  // the experts, ascending, and the entries by expert
+    uint16_t *entry;           // the entries by expert, and room up to a multiple of eight
     uint16_t *owner;           // number in `expert` of each tile
     uint16_t *ordered;
     int16_t *id;               // expert of each entry, -1 for none
+    int *end;                  // sort_entries' (by expert)
+    int *begin, *first;        // entries and tiles of the experts (with entries) before each
+    int *wave_sum;
+    uint16_t *expert;          // the experts with entries, ascending
     int &experts, &bad;
 
     static __host__ __device__ int most(const TokensArgs &a) { return a.E < a.T * a.K ? a.E : a.T * a.K; }
+    static __host__ __device__ int room(const TokensArgs &a) { return (a.T * a.K + 7) / 8 * 8; }
     static __host__ __device__ int bytes(const TokensArgs &a) {
-        return (a.E * 4 + (most(a) + 1) * 8 + (kFewWaves + 2) * 4 + most(a) * 2 + a.T * a.K * 8 + 15) / 16 * 16;
+        return (room(a) * 8 + a.E * 4 + (most(a) + 1) * 8 + (kFewWaves + 2) * 4 + most(a) * 2 + 15) / 16 * 16;
     }
     __device__ __forceinline__ Lists(const TokensArgs &a, char *p)
-        : end(reinterpret_cast<int *>(p)), begin(end + a.E), first(begin + most(a) + 1), wave_sum(first + most(a) + 1),
-          expert(reinterpret_cast<uint16_t *>(wave_sum + kFewWaves + 2)), entry(expert + most(a)), owner(entry + a.T * a.K),
-          ordered(owner + a.T * a.K), id(reinterpret_cast<int16_t *>(ordered + a.T * a.K)), experts(wave_sum[kFewWaves]),
-          bad(wave_sum[kFewWaves + 1]) {}
+        : entry(reinterpret_cast<uint16_t *>(p)), owner(entry + room(a)), ordered(owner + room(a)),
+          id(reinterpret_cast<int16_t *>(ordered + room(a))), end(reinterpret_cast<int *>(id + room(a))), begin(end + a.E),
+          first(begin + most(a) + 1), wave_sum(first + most(a) + 1), expert(reinterpret_cast<uint16_t *>(wave_sum + kFewWaves + 2)),
+          experts(wave_sum[kFewWaves]), bad(wave_sum[kFewWaves + 1]) {}
 
     // Fills them, tiles being of `width` entries at most.  ORDER: an expert's entries lie in ascending order, which they
     // have to where several workgroups take tiles of them.  Called by the whole workgroup; ends with a barrier.
@@ -353,7 +356,12 @@ struct Lists {
                 int rank = p - s;
                 if (m > width) {
                     rank = 0;
-                    for (int q = s; q < s + m; ++q) rank += entry[q] < v;
+                    for (int q = s & ~7; q < s + m; q += 8) {
+                        const u32x4 d = *reinterpret_cast<const u32x4 *>(entry + q);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            rank += q + i >= s && q + i < s + m && static_cast<int>(d[i / 2] >> 16 * (i & 1) & 0xFFFF) < v;
+                    }
                 }
                 ordered[s + rank] = static_cast<uint16_t>(v);
             }
