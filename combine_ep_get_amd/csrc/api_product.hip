@@ -61,8 +61,17 @@ int64_t grad_workspace(const ep_problem *p, const ep_product *q) {
     return 256 + floats * 4;
 }
 
+// The status and the hidden rows.
 int64_t tokens_workspace(const ep_problem *p, const ep_product *q) {
     return 256 + static_cast<int64_t>(p->num_tokens) * p->num_topk * q->out_features * 2;
+}
+
+// Behind them, 256-byte aligned, the entries' rows of a 4-bit layer that keeps them.
+int64_t tokens_rows_offset(const ep_problem *p, const ep_product *q) { return (tokens_workspace(p, q) + 255) / 256 * 256; }
+
+int64_t tokens_workspace_fp4(const ep_problem *p, const ep_product *q) {
+    const int64_t rows = epget::tokens_fp4_rows_bytes(p->num_tokens, p->num_topk, p->num_experts, p->hidden);
+    return rows ? tokens_rows_offset(p, q) + rows : tokens_workspace(p, q);
 }
 
 int check_tokens(const ep_problem *p, const ep_product *q, int32_t multiple) {
@@ -86,8 +95,8 @@ int run_tokens(const ep_problem *p, const ep_product *q, const uint16_t *x, cons
     const int rc = check_tokens(p, q, size_step(type));
     if (rc != EP_OK) return rc;
     const bool scaled = type != epget::kBf16;
-    if (!workspace || !aligned(workspace, 256) || workspace_bytes < static_cast<size_t>(tokens_workspace(p, q)))
-        return EP_ERR_INVALID_ARG;
+    const int64_t need = type == epget::kFp4 ? tokens_workspace_fp4(p, q) : tokens_workspace(p, q);
+    if (!workspace || !aligned(workspace, 256) || workspace_bytes < static_cast<size_t>(need)) return EP_ERR_INVALID_ARG;
     if (p->num_tokens > 0 && (!x || !topk_idx || !w1 || !w2 || !out || (scaled && (!w1_sf || !w2_sf))))
         return EP_ERR_INVALID_ARG;
     if (!aligned16(x, w1, b1, w2, b2, residual, out) || !aligned(topk_idx, 4) || !aligned(topk_weights, 4) ||
@@ -114,6 +123,7 @@ int run_tokens(const ep_problem *p, const ep_product *q, const uint16_t *x, cons
     a.out = out;
     a.status = static_cast<int32_t *>(workspace);
     a.h = reinterpret_cast<uint16_t *>(static_cast<char *>(workspace) + 256);
+    a.y = reinterpret_cast<float *>(static_cast<char *>(workspace) + tokens_rows_offset(p, q));
     if (type == epget::kFp4) return hip_rc(epget::launch_tokens_fp4(a, static_cast<hipStream_t>(stream)));
     return hip_rc(epget::launch_tokens(a, type == epget::kFp8, static_cast<hipStream_t>(stream)));
 }
@@ -238,7 +248,7 @@ int ep_expert_product_backward(const ep_problem *p, const ep_product *q, const u
 }
 
 size_t ep_moe_tokens_workspace_bytes(const ep_problem *p, const ep_product *q) {
-    return check_tokens(p, q, 8) == EP_OK ? static_cast<size_t>(tokens_workspace(p, q)) : 0;
+    return check_tokens(p, q, 8) == EP_OK ? static_cast<size_t>(tokens_workspace_fp4(p, q)) : 0;
 }
 
 int ep_moe_tokens(const ep_problem *p, const ep_product *q, const uint16_t *x, const int32_t *topk_idx,

@@ -309,74 +309,312 @@ __global__ __launch_bounds__(kFewThreads, 2) void product_fp4_kernel(ProductArgs
     }
 }
 
+// Where experts have many columns each, the kernels above would take a weight through the matrix instructions' operands
+// once for 16 of them, and each wave would load its own columns, four times the weight's bytes.  Here a workgroup of
+// four waves works on up to 64 columns and 128 weight rows, 32 a wave; the waves' columns are the same, so each loads a
+// quarter of their stage, 64 k of it, and all read it from LDS.  128 tokens, 8 of 32 experts of 4096 x 2 x 1408: 78 us
+// instead of 133 (an expert's tiles of 32 instead 82); 8 of 8 experts 45 instead of 95.  Bound by the latency of a stage: two
+// are on their way, and registers leave room for two workgroups a CU.
+constexpr int kManyThreads = 256;
+constexpr int kManyWaves = kManyThreads / 64;
+constexpr int kManyColumns = 64;
+constexpr int kManyShared = kManyColumns * kStageK * 2;  // bytes
+
+// This lane's share of a stage: CF fragments of columns.
+template <int CF>
+struct ManyStage {
+    u32x4 w[2][2], x[2 * CF];
+    uint32_t sf[2];
+};
+
+struct ManyRows {
+    const char *w[2], *sf[2], *x;
+    uint32_t w_at[2], sf_at, x_at[kManyColumns / 8];
+};
+
+__device__ __forceinline__ void set_many(ManyRows &r, const Rows<2, 8> &w) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) r.w[i] = w.w[i], r.sf[i] = w.sf[i], r.w_at[i] = w.w_at[i];
+    r.sf_at = w.sf_at;
+}
+
+template <bool FULL, int CF>
+__device__ __forceinline__ void load_many(ManyStage<CF> &s, const ManyRows &r, int b, int K, int wave, const Lanes &ll) {
+    const int64_t w_off = static_cast<int64_t>(b) * (kStageK / 2), sf_off = static_cast<int64_t>(b) * (kStageK / 32);
+#pragma unroll
+    for (int f = 0; f < 2; ++f) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+            s.w[f][h] = FULL || b * kStageK + (ll.piece ^ h) * 32 < K
+                            ? *reinterpret_cast<const u32x4 *>(r.w[f] + w_off + r.w_at[h])
+                            : u32x4{0, 0, 0, 0};
+        const char *p = r.sf[f] + sf_off;
+        if constexpr (FULL) {
+            __builtin_memcpy(&s.sf[f], p + r.sf_at, 4);  // at any address
+        } else {
+            s.sf[f] = 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (b * kStageK + ((__lane_id() & 1) * 4 + i) * 32 < K) s.sf[f] |= uint32_t{static_cast<uint8_t>(p[r.sf_at + i])} << 8 * i;
+        }
+    }
+    const char *x = r.x + static_cast<int64_t>(b) * (kStageK * 2) + wave * 128;
+#pragma unroll
+    for (int h = 0; h < 2 * CF; ++h)
+        s.x[h] = FULL || b * kStageK + wave * 64 + (ll.piece ^ (h & 1)) * 8 < K ? *reinterpret_cast<const u32x4 *>(x + r.x_at[h])
+                                                                               : u32x4{0, 0, 0, 0};
+}
+
+// acc += W rows x columns; the loads of two stages are on their way.  Called by the whole workgroup.
+template <int CF>
+__device__ __forceinline__ void accumulate_many(f32x4 (&acc)[2][kManyColumns / 16], const ManyRows &r, int K, char *shared,
+                                                char *scratch, int wave, const Lanes &ll) {
+    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+    const int full = K / kStageK, all = (K + kStageK - 1) / kStageK;
+    const int lane16 = __lane_id() * 16;
+    const int w_row = (ll.li >> 3) * 1024 + (ll.li & 7) * 128;
+    const char *x_row = shared + (ll.lg >> 1) * (2 * CF * 1024) + w_row;
+    ManyStage<CF> s[2];
+    auto load = [&](ManyStage<CF> &d, int b) {
+        if (b < full)
+            load_many<true>(d, r, b, K, wave, ll);
+        else if (b < all)
+            load_many<false>(d, r, b, K, wave, ll);
+    };
+    auto step = [&](ManyStage<CF> &d, auto &&load_next) {
+        __syncthreads();  // the stage before has been read
+#pragma unroll
+        for (int h = 0; h < 2 * CF; ++h) *reinterpret_cast<u32x4 *>(shared + (wave * 2 * CF + h) * 1024 + lane16) = d.x[h];
+#pragma unroll
+        for (int f = 0; f < 2; ++f)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) *reinterpret_cast<u32x4 *>(scratch + (f * 2 + h) * 1024 + lane16) = d.w[f][h];
+        const uint32_t sf[2] = {d.sf[0], d.sf[1]};
+        load_next(d);
+        __syncthreads();
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            u32x4 w[2];
+            float scale[2];
+#pragma unroll
+            for (int f = 0; f < 2; ++f) {
+                w[f] = *reinterpret_cast<const u32x4 *>(scratch + f * 2048 + w_row + place_of(ll.li, 4 * q + ll.lg) * 16);
+                const uint32_t four = __builtin_amdgcn_ds_bpermute((ll.li * 4 + q) * 4, sf[f]);
+                scale[f] = __uint_as_float((four >> 8 * ll.lg & 255) << 23);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                bf16x8 x[CF];
+#pragma unroll
+                for (int c = 0; c < CF; ++c)
+                    x[c] = *reinterpret_cast<const bf16x8 *>(x_row + (2 * q * 2 * CF + c * 2) * 1024 +
+                                                             place_of(ll.li, (ll.lg & 1) * 4 + i) * 16);
+#pragma unroll
+                for (int f = 0; f < 2; ++f) {
+                    const bf16x2 o0 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w[f][i], scale[f], 0);
+                    const bf16x2 o1 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w[f][i], scale[f], 1);
+                    const bf16x2 o2 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w[f][i], scale[f], 2);
+                    const bf16x2 o3 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w[f][i], scale[f], 3);
+                    const bf16x8 o = {o0[0], o0[1], o1[0], o1[1], o2[0], o2[1], o3[0], o3[1]};
+#pragma unroll
+                    for (int c = 0; c < CF; ++c) acc[f][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(o, x[c], acc[f][c], 0, 0, 0);
+                }
+            }
+        }
+    };
+    int b = 0;  // the stage in s[0]
+    if (full >= 2) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            load_many<true>(s[i], r, i, K, wave, ll);
+            __builtin_amdgcn_sched_barrier(0);  // in this order, as the loop below waits for them
+        }
+        for (; b + 4 <= full; b += 2) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) step(s[i], [&](ManyStage<CF> &d) { load_many<true>(d, r, b + i + 2, K, wave, ll); });
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) step(s[i], [&](ManyStage<CF> &d) { load(d, b + i + 2); });
+        b += 2;
+    } else {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) load(s[i], i);
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+        if (b + i < all) step(s[i], [](ManyStage<CF> &) {});
+}
+
+__device__ __forceinline__ void accumulate_columns(f32x4 (&acc)[2][kManyColumns / 16], const ManyRows &r, int columns, int K,
+                                                   char *shared, char *scratch, int wave, const Lanes &ll) {
+#pragma unroll
+    for (int f = 0; f < 2; ++f)
+#pragma unroll
+        for (int c = 0; c < kManyColumns / 16; ++c) acc[f][c] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    if (columns > 32)
+        accumulate_many<4>(acc, r, K, shared, scratch, wave, ll);
+    else
+        accumulate_many<2>(acc, r, K, shared, scratch, wave, ll);
+}
+
+template <int ACT>
+__global__ __launch_bounds__(kManyThreads, 2) void product_fp4_many_kernel(ProductArgs a) {
+    constexpr bool GATED = act_gated(ACT);
+    constexpr int kOut = item_outputs(GATED, 2), kGroup = kManyWaves * kOut;
+    __shared__ __attribute__((aligned(16))) char shared[kManyShared], scratch[kManyWaves][4096];
+    __shared__ int first[EP_MAX_EXPERTS + 1];
+    __shared__ int wave_sum[kManyWaves];
+    tile_prefix<kManyThreads>(a.seg, kManyColumns, first, wave_sum);
+    const Lanes ll;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int nf = (a.N + kGroup - 1) / kGroup;
+    const int64_t items = static_cast<int64_t>(first[a.seg.E]) * nf;
+    for (int64_t round = 0; round * gridDim.x < items; ++round) {
+        const int64_t item = tile_of(items, round, blockIdx.x, gridDim.x);
+        if (item < 0) break;
+        const int e = tile_expert(first, a.seg.E, static_cast<int>(item / nf));
+        const int f0 = __builtin_amdgcn_readfirstlane(first[e]);
+        const int nt = __builtin_amdgcn_readfirstlane(first[e + 1]) - f0;
+        int tt, ft;
+        tile_in_expert(item - static_cast<int64_t>(f0) * nf, nt, nf, &tt, &ft);
+        int64_t row0;
+        const int rows = segment(a.seg, e, &row0), t0 = tt * kManyColumns;
+        const int place = ft * kGroup + wave * kOut, n0 = min(place, a.N - kOut);
+        Rows<2, 8> w;
+        set_weights(w, a.weight, a.w_sf, e, a.M, a.C, {n0, GATED ? a.N + n0 : n0 + 16}, ll);
+        ManyRows r;
+        set_many(r, w);
+        r.x = reinterpret_cast<const char *>(static_cast<const uint16_t *>(a.x) + (row0 + t0) * a.C);
+#pragma unroll
+        for (int h = 0; h < kManyColumns / 8; ++h)
+            r.x_at[h] = static_cast<uint32_t>(min(h * 8 + ll.row, rows - 1 - t0)) * a.C * 2 + (ll.piece ^ (h & 1)) * 16;
+        f32x4 acc[2][kManyColumns / 16];
+        accumulate_columns(acc, r, rows - t0, a.C, shared, scratch[wave], wave, ll);
+        if (place != n0) continue;  // past the last output
+#pragma unroll
+        for (int c = 0; c < kManyColumns / 16; ++c) {
+            const int t = t0 + c * 16 + ll.li;
+            f32x4 v[1] = {acc[0][c]}, u[1] = {acc[1][c]};
+            if (t < rows) {
+                write_outputs<ACT>(a, e, row0 + t, n0 + ll.lg * 4, v, u);
+                if (!GATED) write_outputs<ACT>(a, e, row0 + t, n0 + ll.lg * 4 + 16, u, u);
+            }
+        }
+    }
+}
+
 // The entries by expert and their tiles, in LDS that the launch sizes.
 struct Lists {
-    uint16_t *entry;           // the entries by expert, and room up to a multiple of eight
-    uint16_t *owner;           // number in `expert` of each tile
-    uint16_t *ordered;
-    int16_t *id;               // expert of each entry, -1 for none
-    int *end;                  // sort_entries' (by expert)
-    int *begin, *first;        // entries and tiles of the experts (with entries) before each
+    int *start;                // entries of the experts before each
+    int *begin, *first;        // the same, and tiles, of the experts with entries
     int *wave_sum;
     uint16_t *expert;          // the experts with entries, ascending
+    uint16_t *entry;           // the entries by expert, ascending in each
+    uint16_t *owner;           // number in `expert` of each tile
+    uint16_t *rank;            // of an entry of a wave's among its expert's, kNone where it is left out
+    int16_t *id;               // expert of each entry, -1 for none
     int &experts, &bad;
+    static constexpr uint16_t kNone = 0xFFFF;
 
     static __host__ __device__ int most(const TokensArgs &a) { return a.E < a.T * a.K ? a.E : a.T * a.K; }
-    static __host__ __device__ int room(const TokensArgs &a) { return (a.T * a.K + 7) / 8 * 8; }
     static __host__ __device__ int bytes(const TokensArgs &a) {
-        return (room(a) * 8 + a.E * 4 + (most(a) + 1) * 8 + (kFewWaves + 2) * 4 + most(a) * 2 + 15) / 16 * 16;
+        return (a.E * 4 + (most(a) + 1) * 8 + (2 * kFewWaves + 2) * 4 + most(a) * 2 + a.T * a.K * 8 + 15) / 16 * 16;
     }
     __device__ __forceinline__ Lists(const TokensArgs &a, char *p)
-        : entry(reinterpret_cast<uint16_t *>(p)), owner(entry + room(a)), ordered(owner + room(a)),
-          id(reinterpret_cast<int16_t *>(ordered + room(a))), end(reinterpret_cast<int *>(id + room(a))), begin(end + a.E),
-          first(begin + most(a) + 1), wave_sum(first + most(a) + 1), expert(reinterpret_cast<uint16_t *>(wave_sum + kFewWaves + 2)),
-          experts(wave_sum[kFewWaves]), bad(wave_sum[kFewWaves + 1]) {}
+        : start(reinterpret_cast<int *>(p)), begin(start + a.E), first(begin + most(a) + 1), wave_sum(first + most(a) + 1),
+          expert(reinterpret_cast<uint16_t *>(wave_sum + 2 * kFewWaves + 2)), entry(expert + most(a)), owner(entry + a.T * a.K),
+          rank(owner + a.T * a.K), id(reinterpret_cast<int16_t *>(rank + a.T * a.K)), experts(wave_sum[2 * kFewWaves]),
+          bad(wave_sum[2 * kFewWaves + 1]) {}
 
-    // Fills them, tiles being of `width` entries at most.  ORDER: an expert's entries lie in ascending order, which they
-    // have to where several workgroups take tiles of them.  Called by the whole workgroup; ends with a barrier.
-    template <int NT, bool ORDER>
-    __device__ __forceinline__ void fill(const TokensArgs &a, int width) {
-        if (a.T * a.K <= 64) {
+    // Fills them, tiles being of `width` entries at most.  An expert's entries are in ascending order, as they have to be
+    // where several workgroups take tiles of them: each wave counts a run of entries, 64 at a time, in a table of its
+    // own in `space`, which nothing else uses meanwhile.  Called by the whole workgroup; ends with a barrier.
+    template <int NT, int N>
+    __device__ __forceinline__ void fill(const TokensArgs &a, int width, char (&space)[N]) {
+        static_assert(N >= NT / 64 * EP_MAX_EXPERTS * 2, "a number of 16 bits for each wave and expert");
+        const int n = a.T * a.K;
+        if (n <= 64) {
             if (threadIdx.x < 64) fill_wave(a, width);
             __syncthreads();
             return;
         }
-        sort_entries<NT>(a, *this);
-        const int per = (experts + NT - 1) / NT;
-        const int i0 = min(static_cast<int>(threadIdx.x) * per, experts), i1 = min(i0 + per, experts);
-        auto start = [&](int e) { return e ? end[e - 1] : 0; };
-        int sum = 0;
-        for (int i = i0; i < i1; ++i) sum += (end[expert[i]] - start(expert[i]) + width - 1) / width;
-        const int incl = wave_inclusive_sum(sum);
-        if ((threadIdx.x & 63) == 63) wave_sum[threadIdx.x >> 6] = incl;
-        const int n = experts ? end[expert[experts - 1]] : 0;
-        if (ORDER) {  // the sort leaves an expert's entries in the order of its atomics
-            for (int p = threadIdx.x; p < n; p += NT) {
-                const int v = entry[p], e = id[v], s = start(e), m = end[e] - s;
-                int rank = p - s;
-                if (m > width) {
-                    rank = 0;
-                    for (int q = s & ~7; q < s + m; q += 8) {
-                        const u32x4 d = *reinterpret_cast<const u32x4 *>(entry + q);
-#pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            rank += q + i >= s && q + i < s + m && static_cast<int>(d[i / 2] >> 16 * (i & 1) & 0xFFFF) < v;
-                    }
-                }
-                ordered[s + rank] = static_cast<uint16_t>(v);
-            }
-            entry = ordered;
+        constexpr int kWaves = NT / 64;
+        const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+        uint16_t *counts = reinterpret_cast<uint16_t *>(space);
+        uint16_t *mine = counts + wave * a.E;
+        for (int i = threadIdx.x; i < kWaves * a.E; i += NT) counts[i] = 0;
+        if (threadIdx.x == 0) bad = 0;
+        __syncthreads();
+        for (int i = threadIdx.x; i < n; i += NT) {
+            const int e = a.idx[i];
+            const bool ok = e >= 0 && e < a.E;
+            id[i] = static_cast<int16_t>(ok ? e : -1);
+            if (!ok && e != -1) bad = 1;
         }
         __syncthreads();
-        int before = incl - sum;
-        for (int w = 0; w < NT / 64; ++w)
-            if (w < static_cast<int>(threadIdx.x >> 6)) before += wave_sum[w];
-        for (int i = i0; i < i1; ++i) {
-            begin[i] = start(expert[i]);
-            first[i] = before;
-            for (int m = end[expert[i]] - begin[i]; m > 0; m -= width) owner[before++] = static_cast<uint16_t>(i);
+        const int run = (n + NT - 1) / NT * 64;
+        auto each = [&](auto f) {  // entries of this wave
+            for (int i = wave * run + lane; i - lane < min((wave + 1) * run, n); i += 64) f(i);
+        };
+        each([&](int i) {
+            const int e = i < n ? id[i] : -1;
+            bool keep = e >= 0;
+            // an entry whose expert the token names before it is left out
+            if (keep)
+                for (int j = i - i % a.K; j < i; ++j) keep = keep && id[j] != e;
+            uint64_t same = __ballot(keep);
+            for (int b = 0; (a.E - 1) >> b; ++b) {
+                const uint64_t set = __ballot(e >> b & 1);
+                same &= e >> b & 1 ? set : ~set;
+            }
+            const int before = __popcll(same & ((uint64_t{1} << lane) - 1));
+            const int base = keep ? mine[e] : 0;
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+            if (keep && before == 0) mine[e] = static_cast<uint16_t>(base + __popcll(same));
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+            if (i < n) rank[i] = keep ? static_cast<uint16_t>(base + before) : kNone;
+        });
+        __syncthreads();
+        // sums over the experts: entries (low half) and experts with any (high half), and tiles
+        const int per = (a.E + NT - 1) / NT;
+        const int e0 = min(static_cast<int>(threadIdx.x) * per, a.E), e1 = min(e0 + per, a.E);
+        int sum = 0, tiles = 0;
+        for (int e = e0; e < e1; ++e) {
+            int m = 0;
+#pragma unroll
+            for (int w = 0; w < kWaves; ++w) {
+                const int c = counts[w * a.E + e];
+                counts[w * a.E + e] = static_cast<uint16_t>(m);
+                m += c;
+            }
+            start[e] = m;
+            sum += m + (m ? 1 << 16 : 0);
+            tiles += (m + width - 1) / width;
         }
-        if (threadIdx.x == NT - 1) first[experts] = before, begin[experts] = n;
+        const int all = wave_inclusive_sum(sum), all_tiles = wave_inclusive_sum(tiles);
+        if (lane == 63) wave_sum[wave] = all, wave_sum[kFewWaves + wave] = all_tiles;
+        __syncthreads();
+        int before = all - sum, tile = all_tiles - tiles;
+        for (int w = 0; w < wave; ++w) before += wave_sum[w], tile += wave_sum[kFewWaves + w];
+        for (int e = e0; e < e1; ++e) {
+            const int m = start[e], i = before >> 16;
+            start[e] = before & 0xFFFF;
+            if (m == 0) continue;
+            expert[i] = static_cast<uint16_t>(e);
+            begin[i] = start[e];
+            first[i] = tile;
+            for (int left = m; left > 0; left -= width) owner[tile++] = static_cast<uint16_t>(i);
+            before += m + (1 << 16);
+        }
+        if (threadIdx.x == NT - 1) {
+            experts = before >> 16;
+            begin[experts] = before & 0xFFFF;
+            first[experts] = tile;
+        }
+        __syncthreads();
+        each([&](int i) {
+            if (i < n && rank[i] != kNone) entry[start[id[i]] + mine[id[i]] + rank[i]] = static_cast<uint16_t>(i);
+        });
         __syncthreads();
     }
 
@@ -430,11 +668,11 @@ template <int ACT, int XC>
 __global__ __launch_bounds__(kFewThreads, 2) void tokens_up_fp4_kernel(TokensArgs a) {
     constexpr bool GATED = act_gated(ACT);
     constexpr int kOut = item_outputs(GATED, 2);
-    __shared__ __attribute__((aligned(16))) char scratch[kFewWaves][kScratch<2, XC>];
+    __shared__ __attribute__((aligned(16))) char scratch[kFewWaves * kScratch<2, XC>];
     __shared__ Part<2> part;
     extern __shared__ __attribute__((aligned(16))) char dynamic[];
     Lists l(a, dynamic);
-    l.fill<kFewThreads, true>(a, XC);
+    l.fill<kFewThreads>(a, XC, scratch);
     if (blockIdx.x == 0 && threadIdx.x == 0) *a.status = l.bad ? EP_ERR_BAD_EXPERT : EP_OK;
     const Lanes ll;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -460,12 +698,54 @@ __global__ __launch_bounds__(kFewThreads, 2) void tokens_up_fp4_kernel(TokensArg
 #pragma unroll
             for (int h = 0; h < XC / 8; ++h)
                 r.x_at[h] = static_cast<uint32_t>(l.entry[s0 + min(c0 + h * 8 + ll.row, m - 1)] / a.K) * a.H * 2 + (ll.piece ^ h) * 16;
-            accumulate<2>(acc, r, a.H, wave % share, share, scratch[wave], ll);
+            accumulate<2>(acc, r, a.H, wave % share, share, scratch + wave * kScratch<2, XC>, ll);
         }
         join(acc, part, wave, share);
         if (item < items && wave % share == 0 && ll.li < XC) {
             up_write<ACT>(a, l, e, c0 + ll.li, m, s0, n0, acc[0], acc[1]);
             if (!GATED) up_write<ACT>(a, l, e, c0 + ll.li, m, s0, n0 + 16, acc[1], acc[1]);
+        }
+    }
+}
+
+template <int ACT>
+__global__ __launch_bounds__(kManyThreads, 2) void tokens_up_fp4_many_kernel(TokensArgs a) {
+    constexpr bool GATED = act_gated(ACT);
+    constexpr int kOut = item_outputs(GATED, 2), kGroup = kManyWaves * kOut;
+    __shared__ __attribute__((aligned(16))) char shared[kManyShared], scratch[kManyWaves][4096];
+    extern __shared__ __attribute__((aligned(16))) char dynamic[];
+    Lists l(a, dynamic);
+    l.fill<kManyThreads>(a, kManyColumns, shared);
+    if (blockIdx.x == 0 && threadIdx.x == 0) *a.status = l.bad ? EP_ERR_BAD_EXPERT : EP_OK;
+    const Lanes ll;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int nf = (a.I + kGroup - 1) / kGroup;
+    const int items = __builtin_amdgcn_readfirstlane(l.first[__builtin_amdgcn_readfirstlane(l.experts)]) * nf;
+    for (int round = 0; round * static_cast<int>(gridDim.x) < items; ++round) {
+        const int item = static_cast<int>(tile_of(items, round, blockIdx.x, gridDim.x));
+        if (item < 0) break;
+        const int i = __builtin_amdgcn_readfirstlane(l.owner[item / nf]);
+        const int f0 = __builtin_amdgcn_readfirstlane(l.first[i]), nt = __builtin_amdgcn_readfirstlane(l.first[i + 1]) - f0;
+        int tt, ft;
+        tile_in_expert(item - f0 * nf, nt, nf, &tt, &ft);
+        const int e = __builtin_amdgcn_readfirstlane(l.expert[i]), c0 = tt * kManyColumns;
+        const int s0 = __builtin_amdgcn_readfirstlane(l.begin[i]), m = __builtin_amdgcn_readfirstlane(l.begin[i + 1]) - s0;
+        const int place = ft * kGroup + wave * kOut, n0 = min(place, a.I - kOut);
+        Rows<2, 8> w;
+        set_weights(w, a.w1, a.w1_sf, e, a.M, a.H, {n0, GATED ? a.I + n0 : n0 + 16}, ll);
+        ManyRows r;
+        set_many(r, w);
+        r.x = reinterpret_cast<const char *>(a.x);
+#pragma unroll
+        for (int h = 0; h < kManyColumns / 8; ++h)
+            r.x_at[h] = static_cast<uint32_t>(l.entry[s0 + min(c0 + h * 8 + ll.row, m - 1)] / a.K) * a.H * 2 + (ll.piece ^ (h & 1)) * 16;
+        f32x4 acc[2][kManyColumns / 16];
+        accumulate_columns(acc, r, m - c0, a.H, shared, scratch[wave], wave, ll);
+        if (place != n0) continue;  // past the last output
+#pragma unroll
+        for (int c = 0; c < kManyColumns / 16; ++c) {
+            up_write<ACT>(a, l, e, c0 + c * 16 + ll.li, m, s0, n0, acc[0][c], acc[1][c]);
+            if (!GATED) up_write<ACT>(a, l, e, c0 + c * 16 + ll.li, m, s0, n0 + 16, acc[1][c], acc[1][c]);
         }
     }
 }
@@ -479,11 +759,11 @@ __global__ __launch_bounds__(kFewThreads, 2) void tokens_up_fp4_kernel(TokensArg
 template <int NT, int XC>
 __global__ __launch_bounds__(NT, 2) void tokens_down_fp4_kernel(TokensArgs a) {
     constexpr int kWaves = NT / 64;
-    __shared__ __attribute__((aligned(16))) char scratch[kWaves][kScratch<1, XC>];
+    __shared__ __attribute__((aligned(16))) char scratch[kWaves * kScratch<1, XC>];
     extern __shared__ __attribute__((aligned(16))) char dynamic[];
     Lists l(a, dynamic);
     float *sums = reinterpret_cast<float *>(dynamic + Lists::bytes(a));
-    l.fill<NT, false>(a, XC);  // a workgroup's own
+    l.fill<NT>(a, XC, scratch);
     const Lanes ll;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int n0 = blockIdx.x * 16;
@@ -505,7 +785,7 @@ __global__ __launch_bounds__(NT, 2) void tokens_down_fp4_kernel(TokensArgs a) {
             r.x_at[h] = static_cast<uint32_t>(l.entry[s0 + min(c0 + h * 8 + ll.row, m - 1)]) * a.I * 2 + (ll.piece ^ h) * 16;
         f32x4 acc[1];
         clear(acc);
-        accumulate<2>(acc, r, a.I, u - t * shares, shares, scratch[wave], ll);
+        accumulate<2>(acc, r, a.I, u - t * shares, shares, scratch + wave * kScratch<1, XC>, ll);
         if (c0 + ll.li < m && ll.li < XC) {
             const int tok = l.entry[s0 + c0 + ll.li] / a.K;
             *reinterpret_cast<f32x4 *>(mine + tok * 16 + ll.lg * 4) += acc[0];
@@ -513,6 +793,90 @@ __global__ __launch_bounds__(NT, 2) void tokens_down_fp4_kernel(TokensArgs a) {
     }
     __syncthreads();
     down_write<1, NT>(a, l, sums, n0);
+}
+
+// down where experts have many entries each: the entries' rows, in 32 bits, whose sums over a token another kernel makes.
+// They are written and read once, 33 MB at 1024 entries of 4096 channels, where each of tokens_down_fp4_kernel's workgroups
+// reads all hidden rows.
+__global__ __launch_bounds__(kManyThreads, 2) void tokens_down_fp4_many_kernel(TokensArgs a) {
+    constexpr int kGroup = kManyWaves * 32;
+    __shared__ __attribute__((aligned(16))) char shared[kManyShared], scratch[kManyWaves][4096];
+    extern __shared__ __attribute__((aligned(16))) char dynamic[];
+    Lists l(a, dynamic);
+    l.fill<kManyThreads>(a, kManyColumns, shared);
+    const Lanes ll;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int nf = (a.H + kGroup - 1) / kGroup;
+    const int items = __builtin_amdgcn_readfirstlane(l.first[__builtin_amdgcn_readfirstlane(l.experts)]) * nf;
+    for (int round = 0; round * static_cast<int>(gridDim.x) < items; ++round) {
+        const int item = static_cast<int>(tile_of(items, round, blockIdx.x, gridDim.x));
+        if (item < 0) break;
+        const int i = __builtin_amdgcn_readfirstlane(l.owner[item / nf]);
+        const int f0 = __builtin_amdgcn_readfirstlane(l.first[i]), nt = __builtin_amdgcn_readfirstlane(l.first[i + 1]) - f0;
+        int tt, ft;
+        tile_in_expert(item - f0 * nf, nt, nf, &tt, &ft);
+        const int e = __builtin_amdgcn_readfirstlane(l.expert[i]), c0 = tt * kManyColumns;
+        const int s0 = __builtin_amdgcn_readfirstlane(l.begin[i]), m = __builtin_amdgcn_readfirstlane(l.begin[i + 1]) - s0;
+        const int place = ft * kGroup + wave * 32, n0 = min(place, a.H - 32);
+        Rows<2, 8> w;
+        set_weights(w, a.w2, a.w2_sf, e, a.H, a.I, {n0, n0 + 16}, ll);
+        ManyRows r;
+        set_many(r, w);
+        r.x = reinterpret_cast<const char *>(a.h);
+#pragma unroll
+        for (int h = 0; h < kManyColumns / 8; ++h)
+            r.x_at[h] = static_cast<uint32_t>(l.entry[s0 + min(c0 + h * 8 + ll.row, m - 1)]) * a.I * 2 + (ll.piece ^ (h & 1)) * 16;
+        f32x4 acc[2][kManyColumns / 16];
+        accumulate_columns(acc, r, m - c0, a.I, shared, scratch[wave], wave, ll);
+        if (place != n0) continue;  // past the last output
+#pragma unroll
+        for (int c = 0; c < kManyColumns / 16; ++c) {
+            const int at = c0 + c * 16 + ll.li;
+            if (at >= m) continue;
+            float *y = a.y + static_cast<int64_t>(l.entry[s0 + at]) * a.H + n0 + ll.lg * 4;
+            *reinterpret_cast<f32x4 *>(y) = acc[0][c];
+            *reinterpret_cast<f32x4 *>(y + 16) = acc[1][c];
+        }
+    }
+}
+
+// Their sums, and what the layer adds to them: a workgroup has kJoinOutputs outputs of a token.
+constexpr int kJoinThreads = 256, kJoinOutputs = kJoinThreads * 4;
+__global__ __launch_bounds__(kJoinThreads) void tokens_join_fp4_kernel(TokensArgs a) {
+    const int t = blockIdx.x, n = blockIdx.y * kJoinOutputs + threadIdx.x * 4, j = threadIdx.x & 63;
+    const int64_t en = static_cast<int64_t>(t) * a.K;
+    const int e = j < a.K ? a.idx[en + j] : -1;
+    const bool ok = e >= 0 && e < a.E;
+    bool keep = ok;  // the first of the token's entries with its expert has the sum of all
+    for (int i = 0; i < a.K; ++i) {
+        const int other = __builtin_amdgcn_readlane(e, i);
+        keep = keep && (i >= j || other != e);
+    }
+    const uint64_t kept = __ballot(keep), valid = __ballot(ok);
+    if (n >= a.H) return;
+    const float *y = a.y + en * a.H + n;
+    f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int j0 = 0; j0 < a.K; j0 += 4) {
+        f32x4 r[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            r[i] = kept >> (j0 + i) & 1 ? *reinterpret_cast<const f32x4 *>(y + static_cast<int64_t>(j0 + i) * a.H) : f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v += r[i];
+    }
+    if (a.b2) {
+        for (uint64_t left = valid; left; left &= left - 1) {
+            const int i = __ffsll(static_cast<unsigned long long>(left)) - 1;
+            const float w = a.w ? a.w[en + i] : 1.0f;
+            v += w * *reinterpret_cast<const f32x4 *>(a.b2 + static_cast<int64_t>(a.idx[en + i]) * a.H + n);
+        }
+    }
+    const int64_t at = static_cast<int64_t>(t) * a.H + n;
+    if (a.residual) {
+        const u32x2 r = *reinterpret_cast<const u32x2 *>(a.residual + at);
+        v += f32x4{bf16_lo(r[0]), bf16_hi(r[0]), bf16_lo(r[1]), bf16_hi(r[1])};
+    }
+    *reinterpret_cast<u32x2 *>(a.out + at) = u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
 }
 
 constexpr int kFp4Workgroups = 256;  // one a CU, which its registers fill
@@ -529,8 +893,22 @@ hipError_t launch_items(const ProductArgs &a, int64_t tiles, hipStream_t stream)
     return hipGetLastError();
 }
 
+// Whether it pays to share columns.  Us without and with it, products of 4096 x 2 x 1408: 7 columns an expert, of 32 experts
+// 66 and 57, of 128 194 and 179; but 8 of 8 experts 20.8 and 23.5, for want of workgroups; 16 of 8 experts 36 and 23, of 4
+// 17.4 and 22.8.  The layer's second product writes its rows for a third kernel, by the same rule: 32 tokens, 8 of 32
+// experts, layers of 107 us without and 101 with it, 128 tokens 191 and 151; 7 of 128 experts 337 and 324.
+bool many(int64_t entries, int64_t E, int64_t outputs, bool gated) {
+    const int64_t group = kManyWaves * item_outputs(gated, 2);
+    const int64_t items = max(entries / kManyColumns, min(E, entries)) * ((outputs + group - 1) / group);
+    return (entries >= 7 * E && items >= 256) || (entries >= 16 * E && items >= 128);
+}
+
 template <int ACT, int XC>
 hipError_t launch_rows(const ProductArgs &a, hipStream_t stream) {
+    if (XC == 16 && many(a.entries, a.seg.E, a.N, act_gated(ACT))) {
+        product_fp4_many_kernel<ACT><<<2 * kFp4Workgroups, kManyThreads, 0, stream>>>(a);
+        return hipGetLastError();
+    }
     const int64_t tiles = a.entries / XC + min(static_cast<int64_t>(a.seg.E), a.entries);  // each expert's last in part filled
     if (tiles * (a.N / item_outputs(act_gated(ACT), 2)) < kFp4Workgroups) return launch_items<ACT, 1, XC>(a, tiles, stream);
     return launch_items<ACT, 2, XC>(a, tiles, stream);
@@ -538,6 +916,10 @@ hipError_t launch_rows(const ProductArgs &a, hipStream_t stream) {
 
 template <int ACT, int XC>
 hipError_t launch_up(const TokensArgs &a, hipStream_t stream) {
+    if (XC == 16 && many(static_cast<int64_t>(a.T) * a.K, a.E, a.I, act_gated(ACT))) {
+        tokens_up_fp4_many_kernel<ACT><<<2 * kFp4Workgroups, kManyThreads, Lists::bytes(a), stream>>>(a);
+        return hipGetLastError();
+    }
     const int64_t entries = static_cast<int64_t>(a.T) * a.K, tiles = entries / XC + min(int64_t{a.E}, entries);
     const int64_t items = max(int64_t{1}, tiles * (a.I / item_outputs(act_gated(ACT), 2)));
     tokens_up_fp4_kernel<ACT, XC><<<min(items, int64_t{kFp4Workgroups}), kFewThreads, Lists::bytes(a), stream>>>(a);
@@ -577,6 +959,11 @@ hipError_t launch_product_fp4(const ProductArgs &a, hipStream_t stream) {
     }
 }
 
+int64_t tokens_fp4_rows_bytes(int32_t T, int32_t K, int32_t E, int32_t H) {
+    const int64_t entries = static_cast<int64_t>(T) * K;
+    return many(entries, E, H, false) ? entries * H * 4 : 0;
+}
+
 hipError_t launch_tokens_fp4(const TokensArgs &a, hipStream_t stream) {
     hipError_t rc = hipErrorInvalidValue;
     const bool wide = wide_tiles(static_cast<int64_t>(a.T) * a.K, a.E);
@@ -593,6 +980,13 @@ hipError_t launch_tokens_fp4(const TokensArgs &a, hipStream_t stream) {
         default: break;
     }
     if (rc != hipSuccess || a.T == 0) return rc;
+    if (many(static_cast<int64_t>(a.T) * a.K, a.E, a.H, false)) {
+        tokens_down_fp4_many_kernel<<<2 * kFp4Workgroups, kManyThreads, Lists::bytes(a), stream>>>(a);
+        if ((rc = hipGetLastError()) != hipSuccess) return rc;
+        const dim3 grid(a.T, (a.H + kJoinOutputs - 1) / kJoinOutputs);
+        tokens_join_fp4_kernel<<<grid, kJoinThreads, 0, stream>>>(a);
+        return hipGetLastError();
+    }
     return wide ? launch_down_rows<16>(a, stream) : launch_down_rows<8>(a, stream);
 }
 

@@ -27,6 +27,11 @@ PRODUCTS = [
     (100, 320, 416, 32, 4, 4, 1, "none", True, True),
     (128, 512, 64, 2, 2, 1, 1, "swiglu", True, True),
     (128, 64, 2048, 300, 8, 2, 1, "silu", False, False),
+    # many rows an expert: tiles of up to 64, whose columns a workgroup's waves share
+    (128, 288, 4160, 2, 2, 1, 1, "swiglu", True, True),
+    (100, 1088, 4128, 4, 4, 2, 1, "none", True, True),
+    (96, 32, 2080, 16, 16, 4, 4, "geglu", False, True),
+    (128, 2304, 1056, 16, 8, 1, 1, "relu", True, False),
 ]
 
 
@@ -120,6 +125,13 @@ TOKENS = [
     (2, 64, 32, 9, 32, "silu", True, True, True, True, 0.3),           # 64 entries: one wave sorts them
     (128, 32, 32, 2048, 32, "relu", True, False, True, False, 0.0),    # the most experts and entries
     (1, 7168, 64, 3, 2, "gelu", False, True, False, False, 0.0),       # more workgroups than CUs
+    # many entries an expert: tiles of up to 64, whose columns a workgroup's waves share, and a third kernel
+    (128, 96, 4128, 2, 2, "swiglu", True, True, True, False, 0.0),     # the first product alone
+    (97, 8224, 96, 2, 2, "gelu", True, True, True, False, 0.1),        # the second alone
+    (128, 2080, 1056, 4, 4, "geglu", True, False, True, False, 0.3),
+    (77, 2080, 2080, 9, 9, "silu", False, True, False, True, 0.1),
+    (128, 8448, 160, 2, 6, "swiglu", True, True, True, True, 0.0),     # every token names an expert many times
+    (16, 1312, 1056, 16, 8, "relu", True, True, True, False, 0.0),
     (28, 64, 96, 8, 2, "swiglu", False, False, True, False, 0.0),      # the fewest entries an expert for tiles of sixteen
 ]
 
@@ -223,6 +235,52 @@ def test_graph_replays(ep):  # noqa: F811
         torch.cuda.synchronize()
         for o in outs:
             assert torch.equal(o, want[n % 2])
+
+
+def many(ep):  # noqa: F811
+    """A layer that both products work on in shared tiles, with a b2 that tells where it was added."""
+    p, q, x, idx, tw, w1, w2, _ = small(ep, T=100, E=4, K=4, H=4128, I=4096)
+    ws = torch.full((ep.ep_moe_tokens_workspace_bytes(p, q),), 255, dtype=torch.uint8, device="cuda")
+    assert ws.numel() >= 256 + 400 * 4096 * 2 + 400 * 4128 * 4
+    return p, q, x, idx, tw, w1, w2, ws, torch.arange(4 * 4128, device="cuda").view(4, 4128) * 2.0 ** -12
+
+
+def test_many_entries_bad_ids_and_values_that_are_not_finite(ep):  # noqa: F811
+    p, q, x, idx, tw, w1, w2, ws, b2 = many(ep)
+    want, out = marked(*x.shape), marked(*x.shape)
+    idx[7, 1], idx[90] = -1, -1
+    ep.ep_moe_tokens_fp4(p, q, x, idx, tw, *w1, None, *w2, b2, x, want, ws)
+    assert ep.ep_read_status(ws) == ep.EP_OK and torch.equal(want[90], x[90])
+    idx[7, 1], idx[90] = 4, -5
+    ep.ep_moe_tokens_fp4(p, q, x, idx, tw, *w1, None, *w2, b2, x, out, ws)
+    assert ep.ep_read_status(ws) == ep.EP_ERR_BAD_EXPERT and torch.equal(out, want)
+    x[5, 3] = float("nan")
+    w1[1][3, 2] = 255
+    idx[:50][idx[:50] == 3] = 1
+    idx[90] = -1
+    ep.ep_moe_tokens_fp4(p, q, x, idx, tw, *w1, None, *w2, b2, x, out, ws)
+    hit = (idx == 3).any(1)
+    hit[5] = True
+    assert torch.isnan(out[hit]).any(1).all() and not torch.isnan(out[~hit]).any() and 0 < int(hit.sum()) < 90
+
+
+def test_many_entries_replayed(ep):  # noqa: F811
+    p, q, x, idx, tw, w1, w2, ws, b2 = many(ep)
+    batches, want = [idx.clone(), idx.flip(0).contiguous(), idx.sort(1).values.contiguous()], []
+    for i in batches:
+        want.append(marked(*x.shape))
+        ep.ep_moe_tokens_fp4(p, q, x, i, tw, *w1, None, *w2, b2, None, want[-1], ws)
+    out, graph = marked(*x.shape), torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        ep.ep_moe_tokens_fp4(p, q, x, idx, tw, *w1, None, *w2, b2, None, out, ws)
+    for n in range(6):
+        idx.copy_(batches[n % 3])
+        out.zero_()
+        ws.fill_(255)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want[n % 3])
 
 
 @pytest.mark.parametrize("T,E", [(128, 1), (128, 2), (100, 5), (60, 4)])
