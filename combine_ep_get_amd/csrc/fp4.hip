@@ -663,99 +663,138 @@ struct Lists {
     }
 };
 
+// The layer's two products as rows of the entries: the hidden rows, and what each entry adds to its token, in 32 bits.
+template <int ACT>
+struct UpRows {
+    static constexpr bool kGated = act_gated(ACT), kFirst = true;
+    static __host__ __device__ int outputs(const TokensArgs &a) { return a.I; }
+    static __device__ int inputs(const TokensArgs &a) { return a.H; }
+    static __device__ int weight_rows(const TokensArgs &a) { return a.M; }
+    static __device__ const void *weight(const TokensArgs &a) { return a.w1; }
+    static __device__ const void *scales(const TokensArgs &a) { return a.w1_sf; }
+    static __device__ const uint16_t *x(const TokensArgs &a) { return a.x; }
+    static __device__ int x_row(const TokensArgs &a, int entry) { return entry / a.K; }
+    // Column c of an expert's m entries from s0 on, outputs n0 .. n0 + 15 (v, and u of the gates' other halves or the next 16).
+    static __device__ __forceinline__ void write(const TokensArgs &a, const Lists &l, int e, int c, int m, int s0, int n0,
+                                                 f32x4 v, f32x4 u) {
+        up_write<ACT>(a, l, e, c, m, s0, n0, v, u);
+        if (!kGated) up_write<ACT>(a, l, e, c, m, s0, n0 + 16, u, u);
+    }
+};
+
+struct DownRows {
+    static constexpr bool kGated = false, kFirst = false;
+    static __host__ __device__ int outputs(const TokensArgs &a) { return a.H; }
+    static __device__ int inputs(const TokensArgs &a) { return a.I; }
+    static __device__ int weight_rows(const TokensArgs &a) { return a.H; }
+    static __device__ const void *weight(const TokensArgs &a) { return a.w2; }
+    static __device__ const void *scales(const TokensArgs &a) { return a.w2_sf; }
+    static __device__ const uint16_t *x(const TokensArgs &a) { return a.h; }
+    static __device__ int x_row(const TokensArgs &, int entry) { return entry; }
+    static __device__ __forceinline__ void write(const TokensArgs &a, const Lists &l, int, int c, int m, int s0, int n0,
+                                                 f32x4 v, f32x4 u) {
+        if (c >= m) return;
+        float *y = a.y + static_cast<int64_t>(l.entry[s0 + c]) * a.H + n0 + (__lane_id() >> 4) * 4;
+        *reinterpret_cast<f32x4 *>(y) = v;
+        *reinterpret_cast<f32x4 *>(y + 16) = u;
+    }
+};
+
+// Tile `tile` of `nf` tiles of outputs for each tile of up to XC entries.
+struct EntryTile {
+    int e, s0, m, c0, ft;  // expert, its first entry, its entries, the tile's first of them, tile of outputs
+    __device__ __forceinline__ EntryTile(const Lists &l, int tile, int nf, int XC) {
+        const int i = __builtin_amdgcn_readfirstlane(l.owner[tile / nf]);
+        const int f0 = __builtin_amdgcn_readfirstlane(l.first[i]), nt = __builtin_amdgcn_readfirstlane(l.first[i + 1]) - f0;
+        int tt;
+        tile_in_expert(tile - f0 * nf, nt, nf, &tt, &ft);
+        e = __builtin_amdgcn_readfirstlane(l.expert[i]);
+        s0 = __builtin_amdgcn_readfirstlane(l.begin[i]);
+        m = __builtin_amdgcn_readfirstlane(l.begin[i + 1]) - s0;
+        c0 = tt * XC;
+    }
+    // Bytes of this lane's row h of the columns and its piece of a line.
+    template <class Side>
+    __device__ __forceinline__ uint32_t x_at(const TokensArgs &a, const Lists &l, int h, const Lanes &ll) const {
+        const int row = Side::x_row(a, l.entry[s0 + min(c0 + h * 8 + ll.row, m - 1)]);
+        return static_cast<uint32_t>(row) * Side::inputs(a) * 2 + (ll.piece ^ (h & 1)) * 16;
+    }
+};
+
 // XC: columns of a tile of entries.
-template <int ACT, int XC>
-__global__ __launch_bounds__(kFewThreads, 2) void tokens_up_fp4_kernel(TokensArgs a) {
-    constexpr bool GATED = act_gated(ACT);
-    constexpr int kOut = item_outputs(GATED, 2);
+template <class Side, int XC>
+__global__ __launch_bounds__(kFewThreads, 2) void tokens_rows_fp4_kernel(TokensArgs a) {
+    constexpr int kOut = item_outputs(Side::kGated, 2);
     __shared__ __attribute__((aligned(16))) char scratch[kFewWaves * kScratch<2, XC>];
     __shared__ Part<2> part;
     extern __shared__ __attribute__((aligned(16))) char dynamic[];
     Lists l(a, dynamic);
     l.fill<kFewThreads>(a, XC, scratch);
-    if (blockIdx.x == 0 && threadIdx.x == 0) *a.status = l.bad ? EP_ERR_BAD_EXPERT : EP_OK;
+    if (Side::kFirst && blockIdx.x == 0 && threadIdx.x == 0) *a.status = l.bad ? EP_ERR_BAD_EXPERT : EP_OK;
     const Lanes ll;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int experts = __builtin_amdgcn_readfirstlane(l.experts);
-    const int nf = a.I / kOut, items = __builtin_amdgcn_readfirstlane(l.first[experts]) * nf;
+    const int N = Side::outputs(a), K = Side::inputs(a);
+    const int nf = N / kOut, items = __builtin_amdgcn_readfirstlane(l.first[__builtin_amdgcn_readfirstlane(l.experts)]) * nf;
     const int share = waves_of_item(items), per = kFewWaves / share;
     for (int g = blockIdx.x; g * per < items; g += gridDim.x) {
         const int item = g * per + wave / share;
         f32x4 acc[2];
         clear(acc);
-        int e = 0, n0 = 0, c0 = 0, s0 = 0, m = 0;
+        const EntryTile t(l, min(item, items - 1), nf, XC);
+        const int n0 = t.ft * kOut;
         if (item < items) {
-            const int i = __builtin_amdgcn_readfirstlane(l.owner[item / nf]);
-            const int f0 = __builtin_amdgcn_readfirstlane(l.first[i]), nt = __builtin_amdgcn_readfirstlane(l.first[i + 1]) - f0;
-            int tt, ft;
-            tile_in_expert(item - f0 * nf, nt, nf, &tt, &ft);
-            e = __builtin_amdgcn_readfirstlane(l.expert[i]);
-            s0 = __builtin_amdgcn_readfirstlane(l.begin[i]), m = __builtin_amdgcn_readfirstlane(l.begin[i + 1]) - s0;
-            n0 = ft * kOut, c0 = tt * XC;
             Rows<2, XC> r;
-            set_weights(r, a.w1, a.w1_sf, e, a.M, a.H, {n0, GATED ? a.I + n0 : n0 + 16}, ll);
-            r.x = reinterpret_cast<const char *>(a.x);
+            set_weights(r, Side::weight(a), Side::scales(a), t.e, Side::weight_rows(a), K, {n0, Side::kGated ? N + n0 : n0 + 16}, ll);
+            r.x = reinterpret_cast<const char *>(Side::x(a));
 #pragma unroll
-            for (int h = 0; h < XC / 8; ++h)
-                r.x_at[h] = static_cast<uint32_t>(l.entry[s0 + min(c0 + h * 8 + ll.row, m - 1)] / a.K) * a.H * 2 + (ll.piece ^ h) * 16;
-            accumulate<2>(acc, r, a.H, wave % share, share, scratch + wave * kScratch<2, XC>, ll);
+            for (int h = 0; h < XC / 8; ++h) r.x_at[h] = t.x_at<Side>(a, l, h, ll);
+            accumulate<2>(acc, r, K, wave % share, share, scratch + wave * kScratch<2, XC>, ll);
         }
         join(acc, part, wave, share);
-        if (item < items && wave % share == 0 && ll.li < XC) {
-            up_write<ACT>(a, l, e, c0 + ll.li, m, s0, n0, acc[0], acc[1]);
-            if (!GATED) up_write<ACT>(a, l, e, c0 + ll.li, m, s0, n0 + 16, acc[1], acc[1]);
-        }
+        if (item < items && wave % share == 0 && ll.li < XC) Side::write(a, l, t.e, t.c0 + ll.li, t.m, t.s0, n0, acc[0], acc[1]);
     }
 }
 
-template <int ACT>
-__global__ __launch_bounds__(kManyThreads, 2) void tokens_up_fp4_many_kernel(TokensArgs a) {
-    constexpr bool GATED = act_gated(ACT);
-    constexpr int kOut = item_outputs(GATED, 2), kGroup = kManyWaves * kOut;
+template <class Side>
+__global__ __launch_bounds__(kManyThreads, 2) void tokens_rows_fp4_many_kernel(TokensArgs a) {
+    constexpr int kOut = item_outputs(Side::kGated, 2), kGroup = kManyWaves * kOut;
     __shared__ __attribute__((aligned(16))) char shared[kManyShared], scratch[kManyWaves][4096];
     extern __shared__ __attribute__((aligned(16))) char dynamic[];
     Lists l(a, dynamic);
     l.fill<kManyThreads>(a, kManyColumns, shared);
-    if (blockIdx.x == 0 && threadIdx.x == 0) *a.status = l.bad ? EP_ERR_BAD_EXPERT : EP_OK;
+    if (Side::kFirst && blockIdx.x == 0 && threadIdx.x == 0) *a.status = l.bad ? EP_ERR_BAD_EXPERT : EP_OK;
     const Lanes ll;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int nf = (a.I + kGroup - 1) / kGroup;
+    const int N = Side::outputs(a), K = Side::inputs(a);
+    const int nf = (N + kGroup - 1) / kGroup;
     const int items = __builtin_amdgcn_readfirstlane(l.first[__builtin_amdgcn_readfirstlane(l.experts)]) * nf;
     for (int round = 0; round * static_cast<int>(gridDim.x) < items; ++round) {
         const int item = static_cast<int>(tile_of(items, round, blockIdx.x, gridDim.x));
         if (item < 0) break;
-        const int i = __builtin_amdgcn_readfirstlane(l.owner[item / nf]);
-        const int f0 = __builtin_amdgcn_readfirstlane(l.first[i]), nt = __builtin_amdgcn_readfirstlane(l.first[i + 1]) - f0;
-        int tt, ft;
-        tile_in_expert(item - f0 * nf, nt, nf, &tt, &ft);
-        const int e = __builtin_amdgcn_readfirstlane(l.expert[i]), c0 = tt * kManyColumns;
-        const int s0 = __builtin_amdgcn_readfirstlane(l.begin[i]), m = __builtin_amdgcn_readfirstlane(l.begin[i + 1]) - s0;
-        const int place = ft * kGroup + wave * kOut, n0 = min(place, a.I - kOut);
+        const EntryTile t(l, item, nf, kManyColumns);
+        const int place = t.ft * kGroup + wave * kOut, n0 = min(place, N - kOut);
         Rows<2, 8> w;
-        set_weights(w, a.w1, a.w1_sf, e, a.M, a.H, {n0, GATED ? a.I + n0 : n0 + 16}, ll);
+        set_weights(w, Side::weight(a), Side::scales(a), t.e, Side::weight_rows(a), K, {n0, Side::kGated ? N + n0 : n0 + 16}, ll);
         ManyRows r;
         set_many(r, w);
-        r.x = reinterpret_cast<const char *>(a.x);
+        r.x = reinterpret_cast<const char *>(Side::x(a));
 #pragma unroll
-        for (int h = 0; h < kManyColumns / 8; ++h)
-            r.x_at[h] = static_cast<uint32_t>(l.entry[s0 + min(c0 + h * 8 + ll.row, m - 1)] / a.K) * a.H * 2 + (ll.piece ^ (h & 1)) * 16;
+        for (int h = 0; h < kManyColumns / 8; ++h) r.x_at[h] = t.x_at<Side>(a, l, h, ll);
         f32x4 acc[2][kManyColumns / 16];
-        accumulate_columns(acc, r, m - c0, a.H, shared, scratch[wave], wave, ll);
+        accumulate_columns(acc, r, t.m - t.c0, K, shared, scratch[wave], wave, ll);
         if (place != n0) continue;  // past the last output
 #pragma unroll
-        for (int c = 0; c < kManyColumns / 16; ++c) {
-            up_write<ACT>(a, l, e, c0 + c * 16 + ll.li, m, s0, n0, acc[0][c], acc[1][c]);
-            if (!GATED) up_write<ACT>(a, l, e, c0 + c * 16 + ll.li, m, s0, n0 + 16, acc[1][c], acc[1][c]);
-        }
+        for (int c = 0; c < kManyColumns / 16; ++c)
+            Side::write(a, l, t.e, t.c0 + c * 16 + ll.li, t.m, t.s0, n0, acc[0][c], acc[1][c]);
     }
 }
 
 // down: one workgroup for each 16 outputs, all experts, each wave whole tiles
 // of entries in turn, or shares of their k where there are fewer tiles than waves;
-// the sums of every token are each wave's own in LDS, joined at the end.  (One
-// stream of stages through all of a wave's tiles, with its loads ahead across the
-// tiles' ends, takes more instructions a stage: 128 tokens of 256 experts 1340
-// us, 1270 without.)
+// the sums of every token are each wave's own in LDS, joined at the end.  One
+// kernel, for few tiles.  (One stream of stages through all of a wave's tiles,
+// with its loads ahead across the tiles' ends, takes more instructions a stage:
+// a layer of 128 tokens over 256 experts 1340 us, 1270 without.)
 template <int NT, int XC>
 __global__ __launch_bounds__(NT, 2) void tokens_down_fp4_kernel(TokensArgs a) {
     constexpr int kWaves = NT / 64;
@@ -795,52 +834,8 @@ __global__ __launch_bounds__(NT, 2) void tokens_down_fp4_kernel(TokensArgs a) {
     down_write<1, NT>(a, l, sums, n0);
 }
 
-// down where experts have many entries each: the entries' rows, in 32 bits, whose sums over a token another kernel makes.
-// They are written and read once, 33 MB at 1024 entries of 4096 channels, where each of tokens_down_fp4_kernel's workgroups
-// reads all hidden rows.
-__global__ __launch_bounds__(kManyThreads, 2) void tokens_down_fp4_many_kernel(TokensArgs a) {
-    constexpr int kGroup = kManyWaves * 32;
-    __shared__ __attribute__((aligned(16))) char shared[kManyShared], scratch[kManyWaves][4096];
-    extern __shared__ __attribute__((aligned(16))) char dynamic[];
-    Lists l(a, dynamic);
-    l.fill<kManyThreads>(a, kManyColumns, shared);
-    const Lanes ll;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int nf = (a.H + kGroup - 1) / kGroup;
-    const int items = __builtin_amdgcn_readfirstlane(l.first[__builtin_amdgcn_readfirstlane(l.experts)]) * nf;
-    for (int round = 0; round * static_cast<int>(gridDim.x) < items; ++round) {
-        const int item = static_cast<int>(tile_of(items, round, blockIdx.x, gridDim.x));
-        if (item < 0) break;
-        const int i = __builtin_amdgcn_readfirstlane(l.owner[item / nf]);
-        const int f0 = __builtin_amdgcn_readfirstlane(l.first[i]), nt = __builtin_amdgcn_readfirstlane(l.first[i + 1]) - f0;
-        int tt, ft;
-        tile_in_expert(item - f0 * nf, nt, nf, &tt, &ft);
-        const int e = __builtin_amdgcn_readfirstlane(l.expert[i]), c0 = tt * kManyColumns;
-        const int s0 = __builtin_amdgcn_readfirstlane(l.begin[i]), m = __builtin_amdgcn_readfirstlane(l.begin[i + 1]) - s0;
-        const int place = ft * kGroup + wave * 32, n0 = min(place, a.H - 32);
-        Rows<2, 8> w;
-        set_weights(w, a.w2, a.w2_sf, e, a.H, a.I, {n0, n0 + 16}, ll);
-        ManyRows r;
-        set_many(r, w);
-        r.x = reinterpret_cast<const char *>(a.h);
-#pragma unroll
-        for (int h = 0; h < kManyColumns / 8; ++h)
-            r.x_at[h] = static_cast<uint32_t>(l.entry[s0 + min(c0 + h * 8 + ll.row, m - 1)]) * a.I * 2 + (ll.piece ^ (h & 1)) * 16;
-        f32x4 acc[2][kManyColumns / 16];
-        accumulate_columns(acc, r, m - c0, a.I, shared, scratch[wave], wave, ll);
-        if (place != n0) continue;  // past the last output
-#pragma unroll
-        for (int c = 0; c < kManyColumns / 16; ++c) {
-            const int at = c0 + c * 16 + ll.li;
-            if (at >= m) continue;
-            float *y = a.y + static_cast<int64_t>(l.entry[s0 + at]) * a.H + n0 + ll.lg * 4;
-            *reinterpret_cast<f32x4 *>(y) = acc[0][c];
-            *reinterpret_cast<f32x4 *>(y + 16) = acc[1][c];
-        }
-    }
-}
-
-// Their sums, and what the layer adds to them: a workgroup has kJoinOutputs outputs of a token.
+// The sums of DownRows' rows over the tokens, and what the layer adds to them: a workgroup has kJoinOutputs outputs of a
+// token.
 constexpr int kJoinThreads = 256, kJoinOutputs = kJoinThreads * 4;
 __global__ __launch_bounds__(kJoinThreads) void tokens_join_fp4_kernel(TokensArgs a) {
     const int t = blockIdx.x, n = blockIdx.y * kJoinOutputs + threadIdx.x * 4, j = threadIdx.x & 63;
@@ -895,12 +890,22 @@ hipError_t launch_items(const ProductArgs &a, int64_t tiles, hipStream_t stream)
 
 // Whether it pays to share columns.  Us without and with it, products of 4096 x 2 x 1408: 7 columns an expert, of 32 experts
 // 66 and 57, of 128 194 and 179; but 8 of 8 experts 20.8 and 23.5, for want of workgroups; 16 of 8 experts 36 and 23, of 4
-// 17.4 and 22.8.  The layer's second product writes its rows for a third kernel, by the same rule: 32 tokens, 8 of 32
-// experts, layers of 107 us without and 101 with it, 128 tokens 191 and 151; 7 of 128 experts 337 and 324.
+// 17.4 and 22.8.  Layers over 32 experts, 32 tokens 112 and 101, 128 tokens 241 and 151.
 bool many(int64_t entries, int64_t E, int64_t outputs, bool gated) {
     const int64_t group = kManyWaves * item_outputs(gated, 2);
     const int64_t items = max(entries / kManyColumns, min(E, entries)) * ((outputs + group - 1) / group);
     return (entries >= 7 * E && items >= 256) || (entries >= 16 * E && items >= 128);
+}
+
+// Whether the layer's second product leaves each entry's rows, which a third kernel sums: many tiles are better spread over
+// the chip one by one than by outputs, of which there are too few for all CUs, or some more than one each.  Us of layers
+// without and with it, of 2048 x 768: 2 tokens of 8 experts 25.1 and 25.1, 4 36.6 and 33.2, 64 tokens over 128 experts 106 and
+// 80; of 4672 x 704 over 64 experts 101 and 85, over 256 450 and 360; of 4096 x 1408, with an output tile for each CU, over 64
+// experts 134 and 138, over 128 289 and 285; a token of 8 experts 18.2 and 20.2.
+bool rows_apart(int64_t entries, int64_t E, int64_t H) {
+    const int64_t tiles = max(min(entries, E), entries / 16), outputs = H / 16;
+    const bool uneven = outputs <= 200 || outputs > kFp4Workgroups;
+    return many(entries, E, H, false) || tiles >= (uneven ? 32 : 128);
 }
 
 template <int ACT, int XC>
@@ -914,16 +919,22 @@ hipError_t launch_rows(const ProductArgs &a, hipStream_t stream) {
     return launch_items<ACT, 2, XC>(a, tiles, stream);
 }
 
-template <int ACT, int XC>
-hipError_t launch_up(const TokensArgs &a, hipStream_t stream) {
-    if (XC == 16 && many(static_cast<int64_t>(a.T) * a.K, a.E, a.I, act_gated(ACT))) {
-        tokens_up_fp4_many_kernel<ACT><<<2 * kFp4Workgroups, kManyThreads, Lists::bytes(a), stream>>>(a);
+template <class Side, int XC>
+hipError_t launch_tokens_rows(const TokensArgs &a, hipStream_t stream) {
+    const int64_t entries = static_cast<int64_t>(a.T) * a.K, tiles = entries / XC + min(int64_t{a.E}, entries);
+    const int64_t items = max(int64_t{1}, tiles * (Side::outputs(a) / item_outputs(Side::kGated, 2)));
+    tokens_rows_fp4_kernel<Side, XC><<<min(items, int64_t{kFp4Workgroups}), kFewThreads, Lists::bytes(a), stream>>>(a);
+    return hipGetLastError();
+}
+
+template <class Side>
+hipError_t launch_side(const TokensArgs &a, hipStream_t stream) {
+    const int64_t entries = static_cast<int64_t>(a.T) * a.K;
+    if (many(entries, a.E, Side::outputs(a), Side::kGated)) {
+        tokens_rows_fp4_many_kernel<Side><<<2 * kFp4Workgroups, kManyThreads, Lists::bytes(a), stream>>>(a);
         return hipGetLastError();
     }
-    const int64_t entries = static_cast<int64_t>(a.T) * a.K, tiles = entries / XC + min(int64_t{a.E}, entries);
-    const int64_t items = max(int64_t{1}, tiles * (a.I / item_outputs(act_gated(ACT), 2)));
-    tokens_up_fp4_kernel<ACT, XC><<<min(items, int64_t{kFp4Workgroups}), kFewThreads, Lists::bytes(a), stream>>>(a);
-    return hipGetLastError();
+    return wide_tiles(entries, a.E) ? launch_tokens_rows<Side, 16>(a, stream) : launch_tokens_rows<Side, 8>(a, stream);
 }
 
 template <int NT, int XC>
@@ -933,8 +944,7 @@ hipError_t launch_down(const TokensArgs &a, hipStream_t stream) {
 }
 
 // Eight waves a workgroup, or four where there are more workgroups than CUs, so that two fit one: one token of 7168
-// channels and 8 experts 55.9 and 50.4 us, 9 tokens of 3424 channels 43.0 and 47.5.  32 outputs a workgroup were no faster
-// with 128 tokens (1275 and 1278 us).
+// channels and 8 experts 55.9 and 50.4 us, 9 tokens of 3424 channels 43.0 and 47.5.
 template <int XC>
 hipError_t launch_down_rows(const TokensArgs &a, hipStream_t stream) {
     const bool fits = Lists::bytes(a) + kFewWaves * (kScratch<1, XC> + a.T * 16 * 4) <= 160 * 1024;  // a CU's LDS
@@ -961,15 +971,14 @@ hipError_t launch_product_fp4(const ProductArgs &a, hipStream_t stream) {
 
 int64_t tokens_fp4_rows_bytes(int32_t T, int32_t K, int32_t E, int32_t H) {
     const int64_t entries = static_cast<int64_t>(T) * K;
-    return many(entries, E, H, false) ? entries * H * 4 : 0;
+    return rows_apart(entries, E, H) ? entries * H * 4 : 0;
 }
 
 hipError_t launch_tokens_fp4(const TokensArgs &a, hipStream_t stream) {
     hipError_t rc = hipErrorInvalidValue;
-    const bool wide = wide_tiles(static_cast<int64_t>(a.T) * a.K, a.E);
     switch (a.act) {
 #define EP_ACT_CASE(A) \
-    case A: rc = wide ? launch_up<A, 16>(a, stream) : launch_up<A, 8>(a, stream); break;
+    case A: rc = launch_side<UpRows<A>>(a, stream); break;
         EP_ACT_CASE(EP_ACT_NONE)
         EP_ACT_CASE(EP_ACT_RELU)
         EP_ACT_CASE(EP_ACT_GELU)
@@ -980,14 +989,14 @@ hipError_t launch_tokens_fp4(const TokensArgs &a, hipStream_t stream) {
         default: break;
     }
     if (rc != hipSuccess || a.T == 0) return rc;
-    if (many(static_cast<int64_t>(a.T) * a.K, a.E, a.H, false)) {
-        tokens_down_fp4_many_kernel<<<2 * kFp4Workgroups, kManyThreads, Lists::bytes(a), stream>>>(a);
-        if ((rc = hipGetLastError()) != hipSuccess) return rc;
+    const int64_t entries = static_cast<int64_t>(a.T) * a.K;
+    if (rows_apart(entries, a.E, a.H)) {
+        if ((rc = launch_side<DownRows>(a, stream)) != hipSuccess) return rc;
         const dim3 grid(a.T, (a.H + kJoinOutputs - 1) / kJoinOutputs);
         tokens_join_fp4_kernel<<<grid, kJoinThreads, 0, stream>>>(a);
         return hipGetLastError();
     }
-    return wide ? launch_down_rows<16>(a, stream) : launch_down_rows<8>(a, stream);
+    return wide_tiles(entries, a.E) ? launch_down_rows<16>(a, stream) : launch_down_rows<8>(a, stream);
 }
 
 }  // namespace epget

@@ -652,9 +652,9 @@ int ep_expert_product_fp4(const ep_problem *problem, const ep_product *product, 
 
 /* ep_moe_tokens with weights of that format: w1_fp4 [E,M,H/2] with w1_sf
  * [E,M,H/32], and w2_fp4 [E,H,I/2] with w2_sf [E,H,I/32].  H and I are
- * multiples of 32.  Where experts have many tokens each, the workspace also
- * holds the T * K rows of the second product in fp32, and a third kernel sums
- * them. */
+ * multiples of 32.  Where the tokens reach many experts or an expert has many, the
+ * workspace also holds the T * K rows of the second product in fp32, and a
+ * third kernel sums them; ep_moe_tokens_workspace_bytes counts them. */
 int ep_moe_tokens_fp4(const ep_problem *problem, const ep_product *product, const uint16_t *x,
                       const int32_t *topk_idx, const float *topk_weights, const uint8_t *w1_fp4,
                       const uint8_t *w1_sf, const float *b1, const uint8_t *w2_fp4,
