@@ -70,7 +70,8 @@ int64_t tokens_workspace(const ep_problem *p, const ep_product *q) {
 int64_t tokens_rows_offset(const ep_problem *p, const ep_product *q) { return (tokens_workspace(p, q) + 255) / 256 * 256; }
 
 int64_t tokens_workspace_fp4(const ep_problem *p, const ep_product *q) {
-    const int64_t rows = epget::tokens_fp4_rows_bytes(p->num_tokens, p->num_topk, p->num_experts, p->hidden);
+    const int64_t rows =
+        epget::tokens_fp4_rows_bytes(p->num_tokens, p->num_topk, p->num_experts, p->hidden, q->out_features);
     return rows ? tokens_rows_offset(p, q) + rows : tokens_workspace(p, q);
 }
 

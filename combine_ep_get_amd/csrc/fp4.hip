@@ -901,11 +901,12 @@ bool many(int64_t entries, int64_t E, int64_t outputs, bool gated) {
 // the chip one by one than by outputs, of which there are too few for all CUs, or some more than one each.  Us of layers
 // without and with it, of 2048 x 768: 2 tokens of 8 experts 25.1 and 25.1, 4 36.6 and 33.2, 64 tokens over 128 experts 106 and
 // 80; of 4672 x 704 over 64 experts 101 and 85, over 256 450 and 360; of 4096 x 1408, with an output tile for each CU, over 64
-// experts 134 and 138, over 128 289 and 285; a token of 8 experts 18.2 and 20.2.
-bool rows_apart(int64_t entries, int64_t E, int64_t H) {
-    const int64_t tiles = max(min(entries, E), entries / 16), outputs = H / 16;
-    const bool uneven = outputs <= 200 || outputs > kFp4Workgroups;
-    return many(entries, E, H, false) || tiles >= (uneven ? 32 : 128);
+// experts 134 and 138, over 128 289 and 285; a token of 8 experts 18.2 and 20.2.  Few tiles of a long k are as many where outputs are few: a token
+// of 7 experts of 832 x 3136 30.0 and 26.6; but 8 of 2880 x 2880 45.8 and 48.9.
+bool rows_apart(int64_t entries, int64_t E, int64_t H, int64_t I) {
+    const int64_t tiles = max(min(entries, E), entries / 16), stages = tiles * ((I + kStageK - 1) / kStageK);
+    const bool even = H > 16 * 200 && H <= 16 * kFp4Workgroups;
+    return many(entries, E, H, false) || tiles >= 128 || (!even && tiles >= 32) || (H <= 16 * 128 && stages >= 80);
 }
 
 template <int ACT, int XC>
@@ -969,9 +970,9 @@ hipError_t launch_product_fp4(const ProductArgs &a, hipStream_t stream) {
     }
 }
 
-int64_t tokens_fp4_rows_bytes(int32_t T, int32_t K, int32_t E, int32_t H) {
+int64_t tokens_fp4_rows_bytes(int32_t T, int32_t K, int32_t E, int32_t H, int32_t I) {
     const int64_t entries = static_cast<int64_t>(T) * K;
-    return rows_apart(entries, E, H) ? entries * H * 4 : 0;
+    return rows_apart(entries, E, H, I) ? entries * H * 4 : 0;
 }
 
 hipError_t launch_tokens_fp4(const TokensArgs &a, hipStream_t stream) {
@@ -990,7 +991,7 @@ hipError_t launch_tokens_fp4(const TokensArgs &a, hipStream_t stream) {
     }
     if (rc != hipSuccess || a.T == 0) return rc;
     const int64_t entries = static_cast<int64_t>(a.T) * a.K;
-    if (rows_apart(entries, a.E, a.H)) {
+    if (rows_apart(entries, a.E, a.H, a.I)) {
         if ((rc = launch_side<DownRows>(a, stream)) != hipSuccess) return rc;
         const dim3 grid(a.T, (a.H + kJoinOutputs - 1) / kJoinOutputs);
         tokens_join_fp4_kernel<<<grid, kJoinThreads, 0, stream>>>(a);

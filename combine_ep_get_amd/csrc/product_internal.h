@@ -74,7 +74,7 @@ hipError_t launch_product_grad(const ProductGradArgs &a, hipStream_t stream);
 hipError_t launch_tokens(const TokensArgs &a, bool fp8, hipStream_t stream);
 hipError_t launch_product_fp4(const ProductArgs &a, hipStream_t stream);
 // Bytes of TokensArgs::y, or 0 where it is not used.
-int64_t tokens_fp4_rows_bytes(int32_t T, int32_t K, int32_t E, int32_t H);
+int64_t tokens_fp4_rows_bytes(int32_t T, int32_t K, int32_t E, int32_t H, int32_t I);
 hipError_t launch_tokens_fp4(const TokensArgs &a, hipStream_t stream);
 hipError_t launch_combine_backward(const CopyParams &c, const uint16_t *dout, const uint16_t *y, const int32_t *slot,
                                    const float *w, uint16_t *dy, float *dw, hipStream_t stream);

@@ -132,6 +132,7 @@ TOKENS = [
     (77, 2080, 2080, 9, 9, "silu", False, True, False, True, 0.1),
     (128, 8448, 160, 2, 6, "swiglu", True, True, True, True, 0.0),     # every token names an expert many times
     (16, 1312, 1056, 16, 8, "relu", True, True, True, False, 0.0),
+    (1, 96, 2592, 8, 8, "swiglu", True, True, True, False, 0.0),       # of few tiles with a long k
     (40, 160, 288, 40, 3, "swiglu", True, True, True, True, 0.1),      # the rows of many tiles of eight, joined
     (60, 4128, 96, 20, 10, "gelu", True, False, True, False, 0.2),     # of sixteen
     (33, 4096, 64, 130, 8, "relu", False, True, True, True, 0.0),
