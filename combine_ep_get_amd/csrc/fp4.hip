@@ -527,7 +527,7 @@ struct Lists {
           bad(wave_sum[2 * kFewWaves + 1]) {}
 
     // Fills them, tiles being of `width` entries at most.  An expert's entries are in ascending order, as they have to be
-    // where several workgroups take tiles of them: each wave counts a run of entries, 64 at a time, in a table of its
+    // where several workgroups take tiles of them: each wave counts a run of tokens, up to 64 entries at a time, in a table of its
     // own in `space`, which nothing else uses meanwhile.  Called by the whole workgroup; ends with a barrier.
     template <int NT, int N>
     __device__ __forceinline__ void fill(const TokensArgs &a, int width, char (&space)[N]) {
@@ -552,27 +552,27 @@ struct Lists {
             if (!ok && e != -1) bad = 1;
         }
         __syncthreads();
-        const int run = (n + NT - 1) / NT * 64;
-        auto each = [&](auto f) {  // entries of this wave
-            for (int i = wave * run + lane; i - lane < min((wave + 1) * run, n); i += 64) f(i);
+        const int step = 64 - 64 % a.K, run = ((n + step - 1) / step + kWaves - 1) / kWaves * step;  // whole tokens
+        auto each = [&](auto f) {  // entries of this wave, or -1
+            for (int i = wave * run; i < min((wave + 1) * run, n); i += step) f(lane < step && i + lane < n ? i + lane : -1);
         };
+        const uint64_t below = (uint64_t{1} << lane) - 1, token = below & ~((uint64_t{1} << (lane - lane % a.K)) - 1);
         each([&](int i) {
-            const int e = i < n ? id[i] : -1;
-            bool keep = e >= 0;
-            // an entry whose expert the token names before it is left out
-            if (keep)
-                for (int j = i - i % a.K; j < i; ++j) keep = keep && id[j] != e;
-            uint64_t same = __ballot(keep);
+            const int e = i >= 0 ? id[i] : -1;
+            uint64_t same = __ballot(e >= 0);
             for (int b = 0; (a.E - 1) >> b; ++b) {
                 const uint64_t set = __ballot(e >> b & 1);
                 same &= e >> b & 1 ? set : ~set;
             }
-            const int before = __popcll(same & ((uint64_t{1} << lane) - 1));
+            // an entry whose expert the token names before it is left out
+            const bool keep = e >= 0 && !(same & token);
+            same &= __ballot(keep);
+            const int before = __popcll(same & below);
             const int base = keep ? mine[e] : 0;
             __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
             if (keep && before == 0) mine[e] = static_cast<uint16_t>(base + __popcll(same));
             __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-            if (i < n) rank[i] = keep ? static_cast<uint16_t>(base + before) : kNone;
+            if (i >= 0) rank[i] = keep ? static_cast<uint16_t>(base + before) : kNone;
         });
         __syncthreads();
         // sums over the experts: entries (low half) and experts with any (high half), and tiles
@@ -613,7 +613,7 @@ struct Lists {
         }
         __syncthreads();
         each([&](int i) {
-            if (i < n && rank[i] != kNone) entry[start[id[i]] + mine[id[i]] + rank[i]] = static_cast<uint16_t>(i);
+            if (i >= 0 && rank[i] != kNone) entry[start[id[i]] + mine[id[i]] + rank[i]] = static_cast<uint16_t>(i);
         });
         __syncthreads();
     }
