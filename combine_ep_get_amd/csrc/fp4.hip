@@ -313,8 +313,8 @@ __global__ __launch_bounds__(kFewThreads, 2) void product_fp4_kernel(ProductArgs
 // once for 16 of them, and each wave would load its own columns, four times the weight's bytes.  Here a workgroup of
 // four waves works on up to 64 columns and 128 weight rows, 32 a wave; the waves' columns are the same, so each loads a
 // quarter of their stage, 64 k of it, and all read it from LDS.  128 tokens, 8 of 32 experts of 4096 x 2 x 1408: 78 us
-// instead of 133 (an expert's tiles of 32 instead 82); 8 of 8 experts 45 instead of 95.  Bound by the latency of a stage: two
-// are on their way, and registers leave room for two workgroups a CU.
+// instead of 133 (an expert's tiles of 32 instead 82); 8 of 8 experts 45 instead of 95.  Bound by memory with two workgroups a
+// CU, by a wave's chain of LDS reads and matrix instructions with one.  More than two stages on their way: 58 to 60 us.
 constexpr int kManyThreads = 256;
 constexpr int kManyWaves = kManyThreads / 64;
 constexpr int kManyColumns = 64;
@@ -890,7 +890,7 @@ hipError_t launch_items(const ProductArgs &a, int64_t tiles, hipStream_t stream)
 
 // Whether it pays to share columns.  Us without and with it, products of 4096 x 2 x 1408: 7 columns an expert, of 32 experts
 // 66 and 57, of 128 194 and 179; but 8 of 8 experts 20.8 and 23.5, for want of workgroups; 16 of 8 experts 36 and 23, of 4
-// 17.4 and 22.8.  Layers over 32 experts, 32 tokens 112 and 101, 128 tokens 241 and 151.
+// 17.4 and 22.8.  Layers over 32 experts, 32 tokens 112 and 98, 128 tokens 241 and 146.
 bool many(int64_t entries, int64_t E, int64_t outputs, bool gated) {
     const int64_t group = kManyWaves * item_outputs(gated, 2);
     const int64_t items = max(entries / kManyColumns, min(E, entries)) * ((outputs + group - 1) / group);
