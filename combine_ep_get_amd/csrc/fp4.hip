@@ -314,7 +314,7 @@ __global__ __launch_bounds__(kFewThreads, 2) void product_fp4_kernel(ProductArgs
 // four waves works on up to 64 columns and 128 weight rows, 32 a wave; the waves' columns are the same, so each loads a
 // quarter of their stage, 64 k of it, and all read it from LDS.  128 tokens, 8 of 32 experts of 4096 x 2 x 1408: 78 us
 // instead of 133 (an expert's tiles of 32 instead 82); 8 of 8 experts 45 instead of 95.  Bound by memory with two workgroups a
-// CU, by a wave's chain of LDS reads and matrix instructions with one.  More than two stages on their way: 58 to 60 us.
+// CU, by the columns' way through LDS and the barriers with one.  More than two stages on their way: 58 to 60 us.
 constexpr int kManyThreads = 256;
 constexpr int kManyWaves = kManyThreads / 64;
 constexpr int kManyColumns = 64;
