@@ -51,7 +51,9 @@ __global__ __launch_bounds__(kFewThreads) void product_few_kernel(ProductArgs a)
         for (int f = 0; f < FF; ++f) {
             const int64_t r = static_cast<int64_t>(e) * a.M + f * a.N + min(n0 + li, a.N - 1);
             row[f] = static_cast<const char *>(a.weight) + r * pitch;
-            w_sf[f] = FP8 ? static_cast<const float *>(a.w_sf) + (static_cast<int64_t>(e) * (a.M / 128) + (f * a.N + n0) / 128) * (a.C / 128) : nullptr;
+            w_sf[f] = FP8 ? static_cast<const float *>(a.w_sf) +
+                                (static_cast<int64_t>(e) * (a.M / 128) + (f * a.N + n0) / 128) * (a.C / 128)
+                          : nullptr;
             acc[f][0] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
         }
         const int64_t xr = row0 + min(t0 + li, rows - 1);

@@ -20,8 +20,8 @@
 // load's address, so that the writes are linear and the reads of 16 rows spread
 // over the banks.
 //
-// A layer of 128 tokens over 256 experts of 7168 x 2048 takes 1240 to 1260 us in a call, 4.7 TB/s, the rate of a large copy here;
-// of one token and 8 experts 45 us (4.2).  100 rows of tokens by 128 experts of 4096 x 2 x 1408: 200 us, 4.0 TB/s.
+// A layer of 128 tokens over 256 experts of 7168 x 2048 takes 1240 to 1260 us in a call, 4.7 TB/s, the rate of a large
+// copy; of one token and 8 experts 45 us (4.2).  100 rows of tokens by 128 experts of 4096 x 2 x 1408: 200 us, 4.0 TB/s.
 #include <limits.h>
 
 #include "tokens_device.h"
@@ -63,37 +63,59 @@ struct Rows {
     uint32_t w_at[2], sf_at, x_at[XC / 8];
 };
 
-// FULL: no k of the stage is past K, of which there are zeros.
-template <bool FULL, int FF, int XC>
-__device__ __forceinline__ void load_stage(Stage<FF, XC> &s, const Rows<FF, XC> &r, int b, int K, const Lanes &ll) {
+// The weights of stage b.  FULL: no k of it is past K, of which there are zeros.  ONCE: no other wave reads them soon.
+template <bool FULL, bool ONCE, int FF, int XC>
+__device__ __forceinline__ void load_weights(u32x4 (&w)[FF][2], uint32_t (&sf)[FF], const Rows<FF, XC> &r, int b, int K,
+                                             const Lanes &ll) {
     const int64_t w_off = static_cast<int64_t>(b) * (kStageK / 2), sf_off = static_cast<int64_t>(b) * (kStageK / 32);
-    const char *x = r.x + static_cast<int64_t>(b) * (kStageK * 2);
 #pragma unroll
     for (int f = 0; f < FF; ++f) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            const char *p = r.w[f] + w_off;
-            s.w[f][h] = FULL || b * kStageK + (ll.piece ^ h) * 32 < K
-                            ? __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(p + r.w_at[h]))
-                            : u32x4{0, 0, 0, 0};
+            const u32x4 *p = reinterpret_cast<const u32x4 *>(r.w[f] + w_off + r.w_at[h]);
+            w[f][h] = u32x4{0, 0, 0, 0};
+            if (FULL || b * kStageK + (ll.piece ^ h) * 32 < K) w[f][h] = ONCE ? __builtin_nontemporal_load(p) : *p;
         }
-        const char *p = r.sf[f] + sf_off;
+        const char *p = r.sf[f] + sf_off + r.sf_at;
         if constexpr (FULL) {
-            __builtin_memcpy(&s.sf[f], p + r.sf_at, 4);  // at any address
+            __builtin_memcpy(&sf[f], p, 4);  // at any address
         } else {
-            s.sf[f] = 0;
+            const int k = b * kStageK + (__lane_id() & 1) * 128;
+            sf[f] = 0;
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                if (b * kStageK + ((__lane_id() & 1) * 4 + i) * 32 < K) s.sf[f] |= uint32_t{static_cast<uint8_t>(p[r.sf_at + i])} << 8 * i;
+                if (k + i * 32 < K) sf[f] |= uint32_t{static_cast<uint8_t>(p[i])} << 8 * i;
         }
     }
+}
+
+template <bool FULL, int FF, int XC>
+__device__ __forceinline__ void load_stage(Stage<FF, XC> &s, const Rows<FF, XC> &r, int b, int K, const Lanes &ll) {
+    load_weights<FULL, true>(s.w, s.sf, r, b, K, ll);
+    const char *x = r.x + static_cast<int64_t>(b) * (kStageK * 2);
 #pragma unroll
     for (int u = 0; u < 4; ++u)
 #pragma unroll
         for (int h = 0; h < XC / 8; ++h)
-            s.x[u][h] = FULL || b * kStageK + u * 64 + (ll.piece ^ h) * 8 < K
+            s.x[u][h] = FULL || b * kStageK + u * 64 + (ll.piece ^ (h & 1)) * 8 < K
                             ? *reinterpret_cast<const u32x4 *>(x + u * 128 + r.x_at[h])
                             : u32x4{0, 0, 0, 0};
+}
+
+// The scale of this lane's codes of half q of a stage, from the lane that loaded it: e8m0 is fp32's exponent.
+__device__ __forceinline__ float scale_of(uint32_t sf, int q, const Lanes &ll) {
+    const uint32_t four = __builtin_amdgcn_ds_bpermute((ll.li * 4 + q) * 4, sf);
+    return __uint_as_float((four >> 8 * ll.lg & 255) << 23);  // the conversion takes no other bits
+}
+
+// Eight codes as bf16.
+__device__ __forceinline__ bf16x8 widened(uint32_t codes, float scale) {
+    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+    const bf16x2 o0 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, scale, 0);
+    const bf16x2 o1 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, scale, 1);
+    const bf16x2 o2 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, scale, 2);
+    const bf16x2 o3 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, scale, 3);
+    return bf16x8{o0[0], o0[1], o1[0], o1[1], o2[0], o2[1], o3[0], o3[1]};
 }
 
 // Bytes of LDS of a wave: a stage's weights, and half of its k of one fragment of columns.
@@ -104,7 +126,6 @@ constexpr int kScratch = FF * 2048 + XC / 8 * 2048;
 // for matrix instruction i of half q, and the column's operand is read from the same k.
 template <int FF, int XC>
 __device__ __forceinline__ void use_stage(f32x4 (&acc)[FF], const Stage<FF, XC> &s, char *scratch, const Lanes &ll) {
-    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
     const int lane16 = __lane_id() * 16;
     char *xs = scratch + FF * 2048;
     const int xi = XC == 16 ? ll.li : ll.li & 7;  // eight columns are there twice
@@ -130,19 +151,12 @@ __device__ __forceinline__ void use_stage(f32x4 (&acc)[FF], const Stage<FF, XC> 
             x[i] = *reinterpret_cast<const bf16x8 *>(xs + x_row + place_of(xi, (ll.lg & 1) * 4 + i) * 16);
 #pragma unroll
         for (int f = 0; f < FF; ++f) {
-            const u32x4 w = *reinterpret_cast<const u32x4 *>(scratch + f * 2048 + w_row + place_of(ll.li, 4 * q + ll.lg) * 16);
-            // e8m0 is fp32's exponent; the conversion takes no other bits of its scale
-            const uint32_t four = __builtin_amdgcn_ds_bpermute((ll.li * 4 + q) * 4, s.sf[f]);
-            const float scale = __uint_as_float((four >> 8 * ll.lg & 255) << 23);
+            const int at = f * 2048 + w_row + place_of(ll.li, 4 * q + ll.lg) * 16;
+            const u32x4 w = *reinterpret_cast<const u32x4 *>(scratch + at);
+            const float scale = scale_of(s.sf[f], q, ll);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const bf16x2 o0 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w[i], scale, 0);
-                const bf16x2 o1 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w[i], scale, 1);
-                const bf16x2 o2 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w[i], scale, 2);
-                const bf16x2 o3 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w[i], scale, 3);
-                const bf16x8 o = {o0[0], o0[1], o1[0], o1[1], o2[0], o2[1], o3[0], o3[1]};
-                acc[f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(o, x[i], acc[f], 0, 0, 0);
-            }
+            for (int i = 0; i < 4; ++i)
+                acc[f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(widened(w[i], scale), x[i], acc[f], 0, 0, 0);
         }
     }
 }
@@ -313,8 +327,8 @@ __global__ __launch_bounds__(kFewThreads, 2) void product_fp4_kernel(ProductArgs
 // once for 16 of them, and each wave would load its own columns, four times the weight's bytes.  Here a workgroup of
 // four waves works on up to 64 columns and 128 weight rows, 32 a wave; the waves' columns are the same, so each loads a
 // quarter of their stage, 64 k of it, and all read it from LDS.  128 tokens, 8 of 32 experts of 4096 x 2 x 1408: 78 us
-// instead of 133 (an expert's tiles of 32 instead 82); 8 of 8 experts 45 instead of 95.  Bound by memory with two workgroups a
-// CU, by the columns' way through LDS and the barriers with one.  More than two stages on their way: 58 to 60 us.
+// instead of 133 (tiles of 32 columns: 82); 8 of 8 experts 45 instead of 95.  Bound by memory with two workgroups a CU,
+// by the columns' way through LDS and the barriers with one.  More than two stages on their way: 58 to 60 us.
 constexpr int kManyThreads = 256;
 constexpr int kManyWaves = kManyThreads / 64;
 constexpr int kManyColumns = 64;
@@ -327,49 +341,22 @@ struct ManyStage {
     uint32_t sf[2];
 };
 
-struct ManyRows {
-    const char *w[2], *sf[2], *x;
-    uint32_t w_at[2], sf_at, x_at[kManyColumns / 8];
-};
-
-__device__ __forceinline__ void set_many(ManyRows &r, const Rows<2, 8> &w) {
-#pragma unroll
-    for (int i = 0; i < 2; ++i) r.w[i] = w.w[i], r.sf[i] = w.sf[i], r.w_at[i] = w.w_at[i];
-    r.sf_at = w.sf_at;
-}
-
 template <bool FULL, int CF>
-__device__ __forceinline__ void load_many(ManyStage<CF> &s, const ManyRows &r, int b, int K, int wave, const Lanes &ll) {
-    const int64_t w_off = static_cast<int64_t>(b) * (kStageK / 2), sf_off = static_cast<int64_t>(b) * (kStageK / 32);
-#pragma unroll
-    for (int f = 0; f < 2; ++f) {
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-            s.w[f][h] = FULL || b * kStageK + (ll.piece ^ h) * 32 < K
-                            ? *reinterpret_cast<const u32x4 *>(r.w[f] + w_off + r.w_at[h])
-                            : u32x4{0, 0, 0, 0};
-        const char *p = r.sf[f] + sf_off;
-        if constexpr (FULL) {
-            __builtin_memcpy(&s.sf[f], p + r.sf_at, 4);  // at any address
-        } else {
-            s.sf[f] = 0;
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (b * kStageK + ((__lane_id() & 1) * 4 + i) * 32 < K) s.sf[f] |= uint32_t{static_cast<uint8_t>(p[r.sf_at + i])} << 8 * i;
-        }
-    }
+__device__ __forceinline__ void load_many(ManyStage<CF> &s, const Rows<2, kManyColumns> &r, int b, int K, int wave,
+                                          const Lanes &ll) {
+    load_weights<FULL, false>(s.w, s.sf, r, b, K, ll);
     const char *x = r.x + static_cast<int64_t>(b) * (kStageK * 2) + wave * 128;
 #pragma unroll
-    for (int h = 0; h < 2 * CF; ++h)
-        s.x[h] = FULL || b * kStageK + wave * 64 + (ll.piece ^ (h & 1)) * 8 < K ? *reinterpret_cast<const u32x4 *>(x + r.x_at[h])
-                                                                               : u32x4{0, 0, 0, 0};
+    for (int h = 0; h < 2 * CF; ++h) {
+        s.x[h] = u32x4{0, 0, 0, 0};
+        if (FULL || b * kStageK + wave * 64 + (ll.piece ^ (h & 1)) * 8 < K) s.x[h] = *reinterpret_cast<const u32x4 *>(x + r.x_at[h]);
+    }
 }
 
 // acc += W rows x columns; the loads of two stages are on their way.  Called by the whole workgroup.
 template <int CF>
-__device__ __forceinline__ void accumulate_many(f32x4 (&acc)[2][kManyColumns / 16], const ManyRows &r, int K, char *shared,
-                                                char *scratch, int wave, const Lanes &ll) {
-    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ void accumulate_many(f32x4 (&acc)[2][kManyColumns / 16], const Rows<2, kManyColumns> &r, int K,
+                                                char *shared, char *scratch, int wave, const Lanes &ll) {
     const int full = K / kStageK, all = (K + kStageK - 1) / kStageK;
     const int lane16 = __lane_id() * 16;
     const int w_row = (ll.li >> 3) * 1024 + (ll.li & 7) * 128;
@@ -398,9 +385,9 @@ __device__ __forceinline__ void accumulate_many(f32x4 (&acc)[2][kManyColumns / 1
             float scale[2];
 #pragma unroll
             for (int f = 0; f < 2; ++f) {
-                w[f] = *reinterpret_cast<const u32x4 *>(scratch + f * 2048 + w_row + place_of(ll.li, 4 * q + ll.lg) * 16);
-                const uint32_t four = __builtin_amdgcn_ds_bpermute((ll.li * 4 + q) * 4, sf[f]);
-                scale[f] = __uint_as_float((four >> 8 * ll.lg & 255) << 23);
+                const int at = f * 2048 + w_row + place_of(ll.li, 4 * q + ll.lg) * 16;
+                w[f] = *reinterpret_cast<const u32x4 *>(scratch + at);
+                scale[f] = scale_of(sf[f], q, ll);
             }
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -411,13 +398,10 @@ __device__ __forceinline__ void accumulate_many(f32x4 (&acc)[2][kManyColumns / 1
                                                              place_of(ll.li, (ll.lg & 1) * 4 + i) * 16);
 #pragma unroll
                 for (int f = 0; f < 2; ++f) {
-                    const bf16x2 o0 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w[f][i], scale[f], 0);
-                    const bf16x2 o1 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w[f][i], scale[f], 1);
-                    const bf16x2 o2 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w[f][i], scale[f], 2);
-                    const bf16x2 o3 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w[f][i], scale[f], 3);
-                    const bf16x8 o = {o0[0], o0[1], o1[0], o1[1], o2[0], o2[1], o3[0], o3[1]};
+                    const bf16x8 o = widened(w[f][i], scale[f]);
 #pragma unroll
-                    for (int c = 0; c < CF; ++c) acc[f][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(o, x[c], acc[f][c], 0, 0, 0);
+                    for (int c = 0; c < CF; ++c)
+                        acc[f][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(o, x[c], acc[f][c], 0, 0, 0);
                 }
             }
         }
@@ -445,8 +429,9 @@ __device__ __forceinline__ void accumulate_many(f32x4 (&acc)[2][kManyColumns / 1
         if (b + i < all) step(s[i], [](ManyStage<CF> &) {});
 }
 
-__device__ __forceinline__ void accumulate_columns(f32x4 (&acc)[2][kManyColumns / 16], const ManyRows &r, int columns, int K,
-                                                   char *shared, char *scratch, int wave, const Lanes &ll) {
+__device__ __forceinline__ void accumulate_columns(f32x4 (&acc)[2][kManyColumns / 16], const Rows<2, kManyColumns> &r,
+                                                   int columns, int K, char *shared, char *scratch, int wave,
+                                                   const Lanes &ll) {
 #pragma unroll
     for (int f = 0; f < 2; ++f)
 #pragma unroll
@@ -480,10 +465,8 @@ __global__ __launch_bounds__(kManyThreads, 2) void product_fp4_many_kernel(Produ
         int64_t row0;
         const int rows = segment(a.seg, e, &row0), t0 = tt * kManyColumns;
         const int place = ft * kGroup + wave * kOut, n0 = min(place, a.N - kOut);
-        Rows<2, 8> w;
-        set_weights(w, a.weight, a.w_sf, e, a.M, a.C, {n0, GATED ? a.N + n0 : n0 + 16}, ll);
-        ManyRows r;
-        set_many(r, w);
+        Rows<2, kManyColumns> r;
+        set_weights(r, a.weight, a.w_sf, e, a.M, a.C, {n0, GATED ? a.N + n0 : n0 + 16}, ll);
         r.x = reinterpret_cast<const char *>(static_cast<const uint16_t *>(a.x) + (row0 + t0) * a.C);
 #pragma unroll
         for (int h = 0; h < kManyColumns / 8; ++h)
@@ -515,6 +498,8 @@ struct Lists {
     int16_t *id;               // expert of each entry, -1 for none
     int &experts, &bad;
     static constexpr uint16_t kNone = 0xFFFF;
+    static_assert(EP_MOE_TOKENS_MAX * EP_MAX_TOPK < kNone && EP_MAX_EXPERTS <= 32768,
+                  "entries are 16-bit numbers, ids signed ones");
 
     static __host__ __device__ int most(const TokensArgs &a) { return a.E < a.T * a.K ? a.E : a.T * a.K; }
     static __host__ __device__ int bytes(const TokensArgs &a) {
@@ -527,8 +512,8 @@ struct Lists {
           bad(wave_sum[2 * kFewWaves + 1]) {}
 
     // Fills them, tiles being of `width` entries at most.  An expert's entries are in ascending order, as they have to be
-    // where several workgroups take tiles of them: each wave counts a run of tokens, up to 64 entries at a time, in a table of its
-    // own in `space`, which nothing else uses meanwhile.  Called by the whole workgroup; ends with a barrier.
+    // where several workgroups take tiles of them: each wave counts a run of tokens, up to 64 entries at a time, in a table
+    // of its own in `space`, which nothing else uses meanwhile.  Called by the whole workgroup; ends with a barrier.
     template <int NT, int N>
     __device__ __forceinline__ void fill(const TokensArgs &a, int width, char (&space)[N]) {
         static_assert(N >= NT / 64 * EP_MAX_EXPERTS * 2, "a number of 16 bits for each wave and expert");
@@ -674,7 +659,8 @@ struct UpRows {
     static __device__ const void *scales(const TokensArgs &a) { return a.w1_sf; }
     static __device__ const uint16_t *x(const TokensArgs &a) { return a.x; }
     static __device__ int x_row(const TokensArgs &a, int entry) { return entry / a.K; }
-    // Column c of an expert's m entries from s0 on, outputs n0 .. n0 + 15 (v, and u of the gates' other halves or the next 16).
+    // Column c of an expert's m entries from s0 on, outputs n0 .. n0 + 15: v, and u of the gates' other halves or of the
+    // next 16.
     static __device__ __forceinline__ void write(const TokensArgs &a, const Lists &l, int e, int c, int m, int s0, int n0,
                                                  f32x4 v, f32x4 u) {
         up_write<ACT>(a, l, e, c, m, s0, n0, v, u);
@@ -744,14 +730,15 @@ __global__ __launch_bounds__(kFewThreads, 2) void tokens_rows_fp4_kernel(TokensA
         const int n0 = t.ft * kOut;
         if (item < items) {
             Rows<2, XC> r;
-            set_weights(r, Side::weight(a), Side::scales(a), t.e, Side::weight_rows(a), K, {n0, Side::kGated ? N + n0 : n0 + 16}, ll);
+            set_weights(r, Side::weight(a), Side::scales(a), t.e, Side::weight_rows(a), K, {n0, n0 + (Side::kGated ? N : 16)}, ll);
             r.x = reinterpret_cast<const char *>(Side::x(a));
 #pragma unroll
             for (int h = 0; h < XC / 8; ++h) r.x_at[h] = t.x_at<Side>(a, l, h, ll);
             accumulate<2>(acc, r, K, wave % share, share, scratch + wave * kScratch<2, XC>, ll);
         }
         join(acc, part, wave, share);
-        if (item < items && wave % share == 0 && ll.li < XC) Side::write(a, l, t.e, t.c0 + ll.li, t.m, t.s0, n0, acc[0], acc[1]);
+        if (item < items && wave % share == 0 && ll.li < XC)
+            Side::write(a, l, t.e, t.c0 + ll.li, t.m, t.s0, n0, acc[0], acc[1]);
     }
 }
 
@@ -773,10 +760,8 @@ __global__ __launch_bounds__(kManyThreads, 2) void tokens_rows_fp4_many_kernel(T
         if (item < 0) break;
         const EntryTile t(l, item, nf, kManyColumns);
         const int place = t.ft * kGroup + wave * kOut, n0 = min(place, N - kOut);
-        Rows<2, 8> w;
-        set_weights(w, Side::weight(a), Side::scales(a), t.e, Side::weight_rows(a), K, {n0, Side::kGated ? N + n0 : n0 + 16}, ll);
-        ManyRows r;
-        set_many(r, w);
+        Rows<2, kManyColumns> r;
+        set_weights(r, Side::weight(a), Side::scales(a), t.e, Side::weight_rows(a), K, {n0, n0 + (Side::kGated ? N : 16)}, ll);
         r.x = reinterpret_cast<const char *>(Side::x(a));
 #pragma unroll
         for (int h = 0; h < kManyColumns / 8; ++h) r.x_at[h] = t.x_at<Side>(a, l, h, ll);
@@ -854,8 +839,10 @@ __global__ __launch_bounds__(kJoinThreads) void tokens_join_fp4_kernel(TokensArg
     for (int j0 = 0; j0 < a.K; j0 += 4) {
         f32x4 r[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            r[i] = kept >> (j0 + i) & 1 ? *reinterpret_cast<const f32x4 *>(y + static_cast<int64_t>(j0 + i) * a.H) : f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        for (int i = 0; i < 4; ++i) {
+            r[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+            if (kept >> (j0 + i) & 1) r[i] = *reinterpret_cast<const f32x4 *>(y + static_cast<int64_t>(j0 + i) * a.H);
+        }
 #pragma unroll
         for (int i = 0; i < 4; ++i) v += r[i];
     }
@@ -945,11 +932,11 @@ hipError_t launch_down(const TokensArgs &a, hipStream_t stream) {
 }
 
 // Eight waves a workgroup, or four where there are more workgroups than CUs, so that two fit one: one token of 7168
-// channels and 8 experts 55.9 and 50.4 us, 9 tokens of 3424 channels 43.0 and 47.5.
+// channels and 8 experts 55.9 and 50.4 us, 9 tokens of 3424 channels 43.0 and 47.5.  Few tiles (rows_apart) are fewer than
+// 2048 entries, whose lists, with the sums of 128 tokens and the waves' scratch, take 132 of a CU's 160 KB at most.
 template <int XC>
 hipError_t launch_down_rows(const TokensArgs &a, hipStream_t stream) {
-    const bool fits = Lists::bytes(a) + kFewWaves * (kScratch<1, XC> + a.T * 16 * 4) <= 160 * 1024;  // a CU's LDS
-    return a.H > 16 * kFp4Workgroups || !fits ? launch_down<256, XC>(a, stream) : launch_down<512, XC>(a, stream);
+    return a.H > 16 * kFp4Workgroups ? launch_down<256, XC>(a, stream) : launch_down<512, XC>(a, stream);
 }
 
 }  // namespace

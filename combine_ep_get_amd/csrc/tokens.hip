@@ -18,10 +18,78 @@
 // copy reaches 4.7 and a streaming read 5.2.  The down product's workgroups are
 // H / 16: with fewer channels than 2048 they leave CUs idle (64 tokens of 1024
 // channels 2.8 TB/s, of 128 0.5).
+//
+// Every workgroup first sorts the entries by expert in LDS: at most
+// EP_MOE_TOKENS_MAX * EP_MAX_TOPK ids, which stay in L2.  A token that names an
+// expert twice keeps one entry, with the sum of both weights.
 #include "tokens_device.h"
 
 namespace epget {
 namespace {
+
+constexpr int kMaxEntries = EP_MOE_TOKENS_MAX * EP_MAX_TOPK;
+static_assert(kMaxEntries <= 65536 && EP_MAX_EXPERTS <= 32768, "entries are 16-bit numbers, ids signed ones");
+
+struct EntryLists {
+    int end[EP_MAX_EXPERTS];             // end of expert e's run in `entry` (its start is end[e - 1])
+    uint16_t expert[kMaxEntries < EP_MAX_EXPERTS ? kMaxEntries : EP_MAX_EXPERTS];  // experts with entries, ascending
+    int16_t id[kMaxEntries];             // expert of each entry, -1 for none
+    uint16_t entry[kMaxEntries];         // t * K + j, by expert
+    int wave_sum[kFewWaves];
+    int experts;                         // number of experts with entries
+    int bad;
+
+    __device__ __forceinline__ int start(int e) const { return e ? end[e - 1] : 0; }
+};
+
+// Called by the whole workgroup; ends with a barrier.
+__device__ __forceinline__ void sort_entries(const TokensArgs &a, EntryLists &l) {
+    const int n = a.T * a.K;
+    for (int e = threadIdx.x; e < a.E; e += kFewThreads) l.end[e] = 0;
+    if (threadIdx.x == 0) l.bad = 0;
+    __syncthreads();
+    for (int i = threadIdx.x; i < n; i += kFewThreads) {
+        const int e = a.idx[i];
+        const bool ok = e >= 0 && e < a.E;
+        l.id[i] = ok ? e : -1;
+        if (!ok && e != -1) l.bad = 1;
+    }
+    __syncthreads();
+    // an entry whose expert the token names before it is left out
+    auto first_of_token = [&](int i) {
+        const int e = l.id[i];
+        bool keep = e >= 0;
+        for (int j = i - i % a.K; j < i; ++j) keep = keep && l.id[j] != e;
+        return keep;
+    };
+    for (int i = threadIdx.x; i < n; i += kFewThreads)
+        if (first_of_token(i)) atomicAdd(&l.end[l.id[i]], 1);
+    __syncthreads();
+    // exclusive sums of the counts (low half) and of the experts with any (high half)
+    const int per = (a.E + kFewThreads - 1) / kFewThreads;
+    const int e0 = min(static_cast<int>(threadIdx.x) * per, a.E), e1 = min(e0 + per, a.E);
+    int sum = 0;
+    for (int e = e0; e < e1; ++e) sum += l.end[e] + (l.end[e] ? 1 << 16 : 0);
+    const int incl = wave_inclusive_sum(sum);
+    if ((threadIdx.x & 63) == 63) l.wave_sum[threadIdx.x >> 6] = incl;
+    __syncthreads();
+    int before = incl - sum;
+    for (int w = 0; w < kFewWaves; ++w)
+        if (w < static_cast<int>(threadIdx.x >> 6)) before += l.wave_sum[w];
+    for (int e = e0; e < e1; ++e) {
+        const int c = l.end[e];
+        l.end[e] = before & 0xFFFF;
+        if (c) l.expert[before >> 16] = static_cast<uint16_t>(e);
+        before += c + (c ? 1 << 16 : 0);
+    }
+    if (threadIdx.x == kFewThreads - 1) l.experts = before >> 16;
+    __syncthreads();
+    // the order inside a run is the hardware's: every entry is a column of
+    // its own, whose result does not depend on its place
+    for (int i = threadIdx.x; i < n; i += kFewThreads)
+        if (first_of_token(i)) l.entry[atomicAdd(&l.end[l.id[i]], 1)] = static_cast<uint16_t>(i);
+    __syncthreads();
+}
 
 // up: items are (expert with entries, 16 outputs).  With enough items for
 // every wave of the chip, a wave takes an item by itself and waits for no
@@ -44,7 +112,9 @@ __device__ __forceinline__ void up_columns(const TokensArgs &a, const EntryLists
     for (int f = 0; f < FF; ++f) {
         const int64_t r = static_cast<int64_t>(e) * a.M + f * a.I + min(n0 + li, a.I - 1);
         row[f] = static_cast<const char *>(a.w1) + r * pitch;
-        w_sf[f] = FP8 ? static_cast<const float *>(a.w1_sf) + (static_cast<int64_t>(e) * (a.M / 128) + (f * a.I + n0) / 128) * (a.H / 128) : nullptr;
+        w_sf[f] = FP8 ? static_cast<const float *>(a.w1_sf) +
+                            (static_cast<int64_t>(e) * (a.M / 128) + (f * a.I + n0) / 128) * (a.H / 128)
+                      : nullptr;
     }
 #pragma unroll
     for (int c = 0; c < CF; ++c) {
@@ -117,7 +187,9 @@ __device__ __forceinline__ void down_columns(const TokensArgs &a, const EntryLis
     for (int f = 0; f < FF; ++f) {
         const int n = min(n0 + f * 16 + li, a.H - 1);
         row[f] = static_cast<const char *>(a.w2) + (static_cast<int64_t>(e) * a.H + n) * pitch;
-        w_sf[f] = FP8 ? static_cast<const float *>(a.w2_sf) + (static_cast<int64_t>(e) * (a.H / 128) + min(n0 + f * 16, a.H - 1) / 128) * (a.I / 128) : nullptr;
+        w_sf[f] = FP8 ? static_cast<const float *>(a.w2_sf) +
+                            (static_cast<int64_t>(e) * (a.H / 128) + min(n0 + f * 16, a.H - 1) / 128) * (a.I / 128)
+                      : nullptr;
     }
 #pragma unroll
     for (int c = 0; c < CF; ++c) {
