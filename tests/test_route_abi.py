@@ -201,6 +201,17 @@ def test_reference_sees_a_mistake():
             assert_within(got, want, b)
 
 
+def test_fp4_workspace_where_rows_stay_apart():
+    """Many tiles: the workspace also holds an fp32 row for each entry; few: the hidden rows alone."""
+    q = Q(C=256, N=128)
+    for p, rows in ((P(T=63, E=64, K=3, H=256), True), (P(T=5, E=8, K=3, H=256), False)):
+        entries = p.num_tokens * 3
+        hidden = 256 + entries * q.out_features * 2
+        need = ep.ep_moe_tokens_workspace_bytes(p, q)
+        assert need == ((hidden + 255) // 256 * 256 + entries * 256 * 4 if rows else hidden)
+        assert tokens_fp4(p=p, q=q, n=need - 1) == BAD
+
+
 def test_reference_fp4_round_trip():
     g = torch.Generator().manual_seed(4)
     w = torch.randn(6, 96, generator=g)
