@@ -15,6 +15,7 @@
 // experts: statistics of given choices 5 and 5 us.
 #include <limits.h>
 
+#include <algorithm>
 #include <type_traits>
 
 #include "../../include/ep_get.h"
@@ -804,9 +805,15 @@ hipError_t launch_stats(const RouteArgs &a, hipStream_t stream) {
 
 }  // namespace
 
+// An upper bound of what the calls with fewer tokens or choices need too: what is allocated for the longest batch serves
+// every shorter one, though a token has more lanes, and the partials are more, up to few_tokens and past kFewChoices.
 int64_t route_workspace(int32_t T, int32_t E, int32_t K) {
     int64_t G = 0;
-    with_shape(T, E, K, [&](auto l, auto n) { G = stat_workgroups<l(), n()>(T); });
+    auto most = [&](int32_t t, int32_t k) {
+        with_shape(t, E, k, [&](auto l, auto n) { G = std::max<int64_t>(G, stat_workgroups<l(), n()>(t)); });
+    };
+    most(T, K);
+    most(std::min(T, few_tokens(E)), K);
     return 256 + G * (8 + 4 + static_cast<int64_t>(E) * 8);
 }
 

@@ -164,7 +164,8 @@ size_t ep_workspace_bytes(const ep_problem *problem);
 int64_t ep_rank_stride_hint(const ep_problem *problem);
 
 /* Bytes of device workspace that ep_route (with statistics) and
- * ep_balance_loss need, or 0 if the problem or router is invalid. */
+ * ep_balance_loss need, or 0 if the problem or router is invalid.  It never
+ * falls as T or K grows: what the longest batch needs serves the others. */
 size_t ep_route_workspace_bytes(const ep_problem *problem, const ep_router *router);
 
 /* The router, which makes what the layout and the dispatch take.  With the

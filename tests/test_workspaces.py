@@ -1,0 +1,51 @@
+"""Workspace sizes: what the largest call needs serves the smaller ones."""
+import pytest
+import torch
+
+import combine_ep_get_amd as ep
+import route_reference as ref
+from test_product_abi import BAD, P
+from test_route_abi import R, balance, route
+
+TOKENS = [0, 1, 2, 4, 5, 31, 32, 33, 64, 65, 500, 1023, 1024, 1025, 2048, 3000, 4095, 4096, 4097, 8192, 16384, 16385, 70000, 1 << 20]
+
+
+@pytest.mark.parametrize("E", [1, 8, 64, 65, 128, 129, 256, 257, 512, 1000, 2048])
+def test_the_routers_workspace_never_falls(E):
+    ranks = next(r for r in range(1, E + 1) if E % r == 0 and E // r <= 256)
+    need = {}
+    for T in TOKENS:
+        for K in (1, 2, 8, 11, 12, 13, 16, 32):
+            p = P(T=T, E=E, K=K, R=ranks, S=1)
+            need[T, K] = ep.ep_route_workspace_bytes(p, R())
+            assert need[T, K] > 0
+            for fn in (route, balance):
+                assert fn(p=p, n=need[T, K] - 1) == BAD
+    for (T, K), n in need.items():
+        assert all(n >= m for (t, k), m in need.items() if t <= T and k <= K), (T, K)
+    assert max(need.values()) <= 256 + 512 * (12 + 8 * E)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("E,K", [(256, 8), (64, 4), (130, 13)])
+def test_short_batches_in_the_longest_ones_workspace(E, K):
+    """The statistics of every length from one workspace, whatever an earlier call left in it."""
+    g = torch.Generator().manual_seed(E)
+    long, r = P(T=8192, E=E, K=K, R=1, S=1), R()
+    ws = torch.full((ep.ep_route_workspace_bytes(long, r),), 255, dtype=torch.uint8, device="cuda")
+    for T in (8192, 4096, 3000, 1025, 1024, 33, 32, 1, 4097):
+        logits = torch.randn(T, E, generator=g)
+        p = P(T=T, E=E, K=K, R=1, S=1)
+        idx, w = torch.empty(T, K, dtype=torch.int32, device="cuda"), torch.empty(T, K, device="cuda")
+        stats = [torch.empty(E, dtype=torch.int32, device="cuda"), torch.empty(1, dtype=torch.int32, device="cuda"),
+                 torch.empty(E, device="cuda"), torch.empty(2, device="cuda")]
+        ep.ep_route(p, r, logits.cuda(), None, None, idx, w, *stats, ws)
+        choice = ref.choose(0, logits, None, None, K)
+        assert torch.equal(idx.cpu(), choice)
+        want = ref.statistics(0, logits, choice, None, K)
+        for t, name in zip(stats, ("expert_count", "token_count", "prob_sum", "losses")):
+            value, bound = want[name]
+            if name.endswith("count"):
+                assert torch.equal(t.cpu().long(), torch.as_tensor(value).view(-1)), (T, name)
+            else:
+                assert ((t.cpu().double() - value).abs() <= bound).all(), (T, name)
