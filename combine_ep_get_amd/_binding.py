@@ -255,12 +255,17 @@ _DTYPES: dict = {}
 def _dtypes():
     if not _DTYPES:
         import torch
+
+        def with_named(types, name):  # a type that not every torch has
+            t = getattr(torch, name, None)
+            return types if t is None else (*types, t)
+
         _DTYPES.update({
             "int32": (torch.int32,),
             "int64": (torch.int64,),
             "double": (torch.float64,),
-            "e2m1": (torch.uint8, torch.int8, torch.float4_e2m1fn_x2),  # two codes a byte
-            "e8m0": (torch.uint8, torch.int8, torch.float8_e8m0fnu),
+            "e2m1": with_named((torch.uint8, torch.int8), "float4_e2m1fn_x2"),  # two codes a byte
+            "e8m0": with_named((torch.uint8, torch.int8), "float8_e8m0fnu"),
             "float": (torch.float32,),
             "uint8": (torch.uint8, torch.bool),
             "bf16": (torch.bfloat16, torch.int16, torch.uint16),
