@@ -13,6 +13,8 @@
 // Both calls are bound by memory.  2.8 GB of gradients: the sum 480 us (5.9 TB/s), the clipping 1030 us, a read and a write
 // at 5.5 TB/s; together 1515 us with 4096 workgroups, 1538 with 2048.  The clipping's loads and stores are past the caches:
 // 1610 us with ordinary ones.  40 small gradients: 5, 2 and 7 us, launches for the most part.
+#include <algorithm>
+
 #include "../../include/ep_get.h"
 #include "device_common.h"
 #include "grads_internal.h"
@@ -234,13 +236,18 @@ hipError_t for_tables(const ep_grad *grads, int32_t num, F f) {
 
 }  // namespace
 
+// An upper bound of what a part of the list needs too, which is shared among launches in another way: no launch leaves more
+// partial sums than kGradWorkgroups, or than it has pieces.
 int64_t grad_workspace_bytes(const ep_grad *grads, int32_t num) {
-    int64_t partials = 0;
-    (void)for_tables(grads, num, [&](const GradTable &, int G) {
-        partials += G;
-        return hipSuccess;
-    });
-    return 256 + partials * 8;
+    int64_t pieces = 0, filled = 0;
+    for (int32_t i = 0; i < num; ++i) {
+        const int64_t n = pieces_of(grads[i]);
+        pieces += n;
+        filled += n > 0;
+    }
+    // a launch ends at a full table, or at more pieces than it can number
+    const int64_t launches = (filled + kTableSize - 1) / kTableSize + pieces / (INT32_MAX / 2);
+    return 256 + std::min(pieces, launches * kGradWorkgroups) * 8;
 }
 
 hipError_t launch_square_sum(const ep_grad *grads, int32_t num, double *square_sum, void *workspace, hipStream_t stream) {

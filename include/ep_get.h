@@ -663,7 +663,8 @@ int ep_moe_tokens_fp4(const ep_problem *problem, const ep_product *product, cons
                       uint16_t *out, void *workspace, size_t workspace_bytes, void *stream);
 
 /* Bytes of device workspace that ep_grad_square_sum needs, or 0 if a gradient
- * is invalid.  `grads` is a host array, of which num_grads may be 0. */
+ * is invalid.  `grads` is a host array, of which num_grads may be 0.  What a
+ * list needs serves every part of it, and shorter gradients. */
 size_t ep_grad_workspace_bytes(const ep_grad *grads, int32_t num_grads);
 
 /* The global norm of many gradients, and clipping, in two calls, between

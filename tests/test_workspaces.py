@@ -1,11 +1,13 @@
 """Workspace sizes: what the largest call needs serves the smaller ones."""
+import random
+
 import pytest
 import torch
 
 import combine_ep_get_amd as ep
 import route_reference as ref
-from test_product_abi import BAD, P
-from test_route_abi import R, balance, route
+from test_product_abi import A, BAD, P
+from test_route_abi import R, balance, grads, route
 
 TOKENS = [0, 1, 2, 4, 5, 31, 32, 33, 64, 65, 500, 1023, 1024, 1025, 2048, 3000, 4095, 4096, 4097, 8192, 16384, 16385, 70000, 1 << 20]
 
@@ -49,3 +51,42 @@ def test_short_batches_in_the_longest_ones_workspace(E, K):
                 assert torch.equal(t.cpu().long(), torch.as_tensor(value).view(-1)), (T, name)
             else:
                 assert ((t.cpu().double() - value).abs() <= bound).all(), (T, name)
+
+
+def grads_need(counts):
+    array = grads(*[(A, A, n, i % 2, 0) for i, n in counts])
+    need = ep.load().ep_grad_workspace_bytes(array, len(counts))
+    assert ep.load().ep_grad_square_sum(array, len(counts), A, A, need - 1, None) == BAD
+    return need
+
+
+@pytest.mark.parametrize("seed", range(4))
+def test_a_part_of_the_gradients_needs_no_more(seed):
+    """Without some of them (experts that no token reached), and with shorter ones."""
+    r = random.Random(seed)
+    few = [(i, r.randint(1, 9)) for i in range(64)]
+    large = [(i, 200_000_000 + i) for i in range(64, 130)]
+    mixed = [(i, int(2 ** r.uniform(0, 40)) - 1) for i in range(300)]
+    for counts in (few + large, large + few, mixed):
+        whole = grads_need(counts)
+        for _ in range(20):
+            part = [c for c in counts if r.random() < 0.95]
+            assert grads_need(part) <= whole
+            assert grads_need([(i, n - r.randint(0, n)) for i, n in part]) <= whole
+    assert grads_need(few[1:] + large) <= grads_need(few + large)
+
+
+@pytest.mark.gpu
+def test_parts_of_the_gradients_in_the_whole_lists_workspace():
+    """What lies behind the workspace stays, and every sum is that of its list."""
+    g = torch.Generator().manual_seed(1)
+    tensors = [torch.randn(n, generator=g).cuda() for n in [5] * 64 + [300_000] * 70]
+    need = ep.ep_grad_workspace_bytes(ep.Grads.make(tensors))
+    ws = torch.full((need + 4096,), 255, dtype=torch.uint8, device="cuda")
+    square = torch.empty(1, dtype=torch.float64, device="cuda")
+    for left_out in (set(), {0}, set(range(0, 64, 2)), set(range(64, 134)), set(range(134))):
+        part = [t for i, t in enumerate(tensors) if i not in left_out]
+        ep.ep_grad_square_sum(ep.Grads.make(part), square, ws, need)
+        want = sum(float((t.double() ** 2).sum()) for t in part)
+        assert abs(float(square) - want) <= 2.0 ** -40 * want
+    assert (ws[need:] == 255).all()
