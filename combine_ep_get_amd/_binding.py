@@ -36,6 +36,10 @@ EP_ACT_SILU = 3
 EP_ACT_SWIGLU = 4
 EP_ACT_GEGLU = 5
 
+EP_WEIGHTS_BF16 = 0
+EP_WEIGHTS_FP8 = 1
+EP_WEIGHTS_FP4 = 2
+
 EP_SCORE_SOFTMAX = 0
 EP_SCORE_SIGMOID = 1
 
@@ -52,7 +56,7 @@ EXPORTS = ("ep_workspace_bytes", "ep_rank_stride_hint", "ep_get_layout", "ep_dis
            "ep_moe_tokens_workspace_bytes", "ep_moe_tokens", "ep_moe_tokens_fp8",
            "ep_expert_product_fp4", "ep_moe_tokens_fp4", "ep_route_workspace_bytes", "ep_route",
            "ep_balance_loss", "ep_route_backward", "ep_grad_workspace_bytes", "ep_grad_square_sum",
-           "ep_grad_clip")
+           "ep_grad_clip", "ep_moe_tokens_weights_workspace_bytes")
 
 
 class EpError(RuntimeError):
@@ -216,6 +220,8 @@ def load():
         lib.ep_expert_product_backward.argtypes = [P, Q] + [vp] * 12 + [sz, vp]
         lib.ep_moe_tokens_workspace_bytes.restype = sz
         lib.ep_moe_tokens_workspace_bytes.argtypes = [P, Q]
+        lib.ep_moe_tokens_weights_workspace_bytes.restype = sz
+        lib.ep_moe_tokens_weights_workspace_bytes.argtypes = [P, Q, ctypes.c_int32]
         lib.ep_moe_tokens.restype = ctypes.c_int
         lib.ep_moe_tokens.argtypes = [P, Q] + [vp] * 10 + [sz, vp]
         lib.ep_moe_tokens_fp8.restype = ctypes.c_int
@@ -618,7 +624,13 @@ def ep_expert_product_backward(problem, product, dout, pre, x, expert_count, exp
 
 
 def ep_moe_tokens_workspace_bytes(problem: Problem, product: Product) -> int:
+    """Bytes that serve each of the ep_moe_tokens calls of these sizes."""
     return load().ep_moe_tokens_workspace_bytes(ctypes.byref(problem), ctypes.byref(product))
+
+
+def ep_moe_tokens_weights_workspace_bytes(problem: Problem, product: Product, weights: int) -> int:
+    """Bytes that the call on these weights (EP_WEIGHTS_*) needs; 0 if it refuses the sizes."""
+    return load().ep_moe_tokens_weights_workspace_bytes(ctypes.byref(problem), ctypes.byref(product), weights)
 
 
 def _tokens_ptrs(problem, product, x, topk_idx, topk_weights, w1, w1_sf, b1, w2, w2_sf, b2, residual, out, workspace,

@@ -69,7 +69,8 @@ int64_t tokens_workspace(const ep_problem *p, const ep_product *q) {
 // Behind them, 256-byte aligned, the entries' rows of a 4-bit layer that keeps them.
 int64_t tokens_rows_offset(const ep_problem *p, const ep_product *q) { return (tokens_workspace(p, q) + 255) / 256 * 256; }
 
-int64_t tokens_workspace_fp4(const ep_problem *p, const ep_product *q) {
+int64_t tokens_workspace_of(const ep_problem *p, const ep_product *q, epget::WeightType type) {
+    if (type != epget::kFp4) return tokens_workspace(p, q);
     const int64_t rows =
         epget::tokens_fp4_rows_bytes(p->num_tokens, p->num_topk, p->num_experts, p->hidden, q->out_features);
     return rows ? tokens_rows_offset(p, q) + rows : tokens_workspace(p, q);
@@ -96,7 +97,7 @@ int run_tokens(const ep_problem *p, const ep_product *q, const uint16_t *x, cons
     const int rc = check_tokens(p, q, size_step(type));
     if (rc != EP_OK) return rc;
     const bool scaled = type != epget::kBf16;
-    const int64_t need = type == epget::kFp4 ? tokens_workspace_fp4(p, q) : tokens_workspace(p, q);
+    const int64_t need = tokens_workspace_of(p, q, type);
     if (!workspace || !aligned(workspace, 256) || workspace_bytes < static_cast<size_t>(need)) return EP_ERR_INVALID_ARG;
     if (p->num_tokens > 0 && (!x || !topk_idx || !w1 || !w2 || !out || (scaled && (!w1_sf || !w2_sf))))
         return EP_ERR_INVALID_ARG;
@@ -249,7 +250,16 @@ int ep_expert_product_backward(const ep_problem *p, const ep_product *q, const u
 }
 
 size_t ep_moe_tokens_workspace_bytes(const ep_problem *p, const ep_product *q) {
-    return check_tokens(p, q, 8) == EP_OK ? static_cast<size_t>(tokens_workspace_fp4(p, q)) : 0;
+    if (check_tokens(p, q, size_step(epget::kBf16)) != EP_OK) return 0;
+    const bool fp4 = check_tokens(p, q, size_step(epget::kFp4)) == EP_OK;  // the most of all
+    return static_cast<size_t>(tokens_workspace_of(p, q, fp4 ? epget::kFp4 : epget::kBf16));
+}
+
+size_t ep_moe_tokens_weights_workspace_bytes(const ep_problem *p, const ep_product *q, int32_t weights) {
+    static_assert(EP_WEIGHTS_BF16 == epget::kBf16 && EP_WEIGHTS_FP8 == epget::kFp8 && EP_WEIGHTS_FP4 == epget::kFp4);
+    if (weights < EP_WEIGHTS_BF16 || weights > EP_WEIGHTS_FP4) return 0;
+    const auto type = static_cast<epget::WeightType>(weights);
+    return check_tokens(p, q, size_step(type)) == EP_OK ? static_cast<size_t>(tokens_workspace_of(p, q, type)) : 0;
 }
 
 int ep_moe_tokens(const ep_problem *p, const ep_product *q, const uint16_t *x, const int32_t *topk_idx,

@@ -6,7 +6,7 @@
 
 namespace epget {
 
-// Weights as bf16, as e4m3 with one fp32 scale for 128 x 128, or as e2m1 with one e8m0 scale for 32 of a row.
+// Weights as bf16, as e4m3 with one fp32 scale for 128 x 128, or as e2m1 with one e8m0 scale for 32 of a row: EP_WEIGHTS_*.
 enum WeightType { kBf16, kFp8, kFp4 };
 
 // Rows of the experts inside a receive buffer: expert e owns `count[e]` rows

@@ -82,6 +82,11 @@ extern "C" {
 #define EP_ACT_SWIGLU 4 /* silu(gate) * up */
 #define EP_ACT_GEGLU 5  /* gelu(gate) * up */
 
+/* Weights of the few-token layer. */
+#define EP_WEIGHTS_BF16 0 /* ep_moe_tokens */
+#define EP_WEIGHTS_FP8 1  /* ep_moe_tokens_fp8 */
+#define EP_WEIGHTS_FP4 2  /* ep_moe_tokens_fp4 */
+
 /* Scores of the router. */
 #define EP_SCORE_SOFTMAX 0 /* softmax over the experts */
 #define EP_SCORE_SIGMOID 1 /* 1 / (1 + exp(-logit)) */
@@ -593,9 +598,15 @@ int ep_expert_product_backward(const ep_problem *problem, const ep_product *prod
                                uint16_t *dweight, float *dweight_acc, float *dbias,
                                void *workspace, size_t workspace_bytes, void *stream);
 
-/* Bytes of device workspace that the ep_moe_tokens calls need, or 0 if the
- * problem or product is invalid. */
+/* Bytes of device workspace that serve each of the ep_moe_tokens calls that
+ * takes these sizes, or 0 if the problem or product is invalid.  The 4-bit
+ * layer may need many times what the others do. */
 size_t ep_moe_tokens_workspace_bytes(const ep_problem *problem, const ep_product *product);
+
+/* Bytes that the call on these weights needs (EP_WEIGHTS_*), or 0 if it
+ * refuses the problem or product. */
+size_t ep_moe_tokens_weights_workspace_bytes(const ep_problem *problem, const ep_product *product,
+                                             int32_t weights);
 
 /* The whole expert layer for a few tokens (T <= EP_MOE_TOKENS_MAX), from the
  * router's output to the combined rows, in two kernels and without a layout,
@@ -613,7 +624,8 @@ size_t ep_moe_tokens_workspace_bytes(const ep_problem *problem, const ep_product
  *   b1 [E,M], b2 [E,H] fp32 device, or NULL
  *   residual     [T,H] bf16 device, or NULL; may be out
  *   out          [T,H] bf16 device; may be x
- *   workspace    ep_moe_tokens_workspace_bytes bytes, 256-byte aligned; calls
+ *   workspace    ep_moe_tokens_weights_workspace_bytes bytes (of bf16), or
+ *                ep_moe_tokens_workspace_bytes, 256-byte aligned; calls
  *                that may overlap need one each.  Its first word is the
  *                status that ep_read_status returns: EP_ERR_BAD_EXPERT if an
  *                id is outside [0,E) and not -1 (it counts as empty).
@@ -655,7 +667,7 @@ int ep_expert_product_fp4(const ep_problem *problem, const ep_product *product, 
  * [E,M,H/32], and w2_fp4 [E,H,I/2] with w2_sf [E,H,I/32].  H and I are
  * multiples of 32.  Where the tokens reach many experts or an expert has many, the
  * workspace also holds the T * K rows of the second product in fp32, and a
- * third kernel sums them; ep_moe_tokens_workspace_bytes counts them. */
+ * third kernel sums them; both size calls count them. */
 int ep_moe_tokens_fp4(const ep_problem *problem, const ep_product *product, const uint16_t *x,
                       const int32_t *topk_idx, const float *topk_weights, const uint8_t *w1_fp4,
                       const uint8_t *w1_sf, const float *b1, const uint8_t *w2_fp4,

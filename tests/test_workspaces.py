@@ -6,8 +6,8 @@ import torch
 
 import combine_ep_get_amd as ep
 import route_reference as ref
-from test_product_abi import A, BAD, P
-from test_route_abi import R, balance, grads, route
+from test_product_abi import A, BAD, P, Q, tokens, tokens_fp8
+from test_route_abi import R, balance, grads, route, tokens_fp4
 
 TOKENS = [0, 1, 2, 4, 5, 31, 32, 33, 64, 65, 500, 1023, 1024, 1025, 2048, 3000, 4095, 4096, 4097, 8192, 16384, 16385, 70000, 1 << 20]
 
@@ -90,3 +90,50 @@ def test_parts_of_the_gradients_in_the_whole_lists_workspace():
         want = sum(float((t.double() ** 2).sum()) for t in part)
         assert abs(float(square) - want) <= 2.0 ** -40 * want
     assert (ws[need:] == 255).all()
+
+
+def hidden_rows(p, q):
+    """The status and the hidden rows: all that the bf16 and FP8 layers use."""
+    return 256 + p.num_tokens * p.num_topk * q.out_features * 2
+
+
+@pytest.mark.parametrize("sizes", [dict(T=128, E=256, K=8, H=7168), dict(T=5, E=8, K=3, H=256)], ids=("many", "few"))
+def test_the_few_token_layers_workspace_by_its_weights(sizes):
+    p, q = P(S=1, **sizes), Q(C=sizes["H"], N=2048)
+    need = [ep.ep_moe_tokens_weights_workspace_bytes(p, q, w) for w in (ep.EP_WEIGHTS_BF16, ep.EP_WEIGHTS_FP8, ep.EP_WEIGHTS_FP4)]
+    assert need[0] == need[1] == hidden_rows(p, q)
+    assert need[2] == ep.ep_moe_tokens_workspace_bytes(p, q) >= need[0]
+    for fn, n in zip((tokens, tokens_fp8, tokens_fp4), need):
+        assert fn(p=p, q=q, n=n - 1) == BAD
+    for w in (-1, 3):
+        assert ep.ep_moe_tokens_weights_workspace_bytes(p, q, w) == 0
+
+
+def test_sizes_that_only_some_weights_take():
+    """Rows of the 4-bit layer are not counted where it refuses the sizes."""
+    many = dict(T=128, E=256, K=8, S=1)
+    for p, q, takes in ((P(H=7168, **many), Q(C=7168, N=2056), (1, 0, 0)), (P(H=264, **many), Q(C=264, N=2048), (1, 0, 0)),
+                        (P(H=224, **many), Q(C=224, N=2048), (1, 0, 1)), (P(H=260, **many), Q(C=260, N=2048), (0, 0, 0))):
+        need = [ep.ep_moe_tokens_weights_workspace_bytes(p, q, w) for w in range(3)]
+        assert [int(n > 0) for n in need] == list(takes)
+        assert ep.ep_moe_tokens_workspace_bytes(p, q) == max(need)
+        assert need[0] in (0, hidden_rows(p, q))
+
+
+@pytest.mark.gpu
+def test_the_bf16_layer_in_its_own_workspace():
+    """Nothing behind the bytes that its size call names is written."""
+    g = torch.Generator().manual_seed(3)
+    T, H, I, E, K = 64, 256, 128, 64, 4
+    p, q = P(T=T, H=H, E=E, K=K, R=1, S=1), ep.Product.make(H, I, ep.EP_ACT_RELU)
+    x, w1, w2 = (torch.randn(*s, generator=g).bfloat16().cuda() for s in ((T, H), (E, I, H), (E, H, I)))
+    idx = torch.randint(0, E, (T, K), generator=g, dtype=torch.int32).cuda()
+    small, large = ep.ep_moe_tokens_weights_workspace_bytes(p, q, ep.EP_WEIGHTS_BF16), ep.ep_moe_tokens_workspace_bytes(p, q)
+    assert small == hidden_rows(p, q) < large
+    outs = []
+    for n in (small, large):
+        ws = torch.full((large,), 255, dtype=torch.uint8, device="cuda")
+        outs.append(torch.empty_like(x))
+        ep.ep_moe_tokens(p, q, x, idx, None, w1, None, w2, None, None, outs[-1], ws, n)
+        assert ep.ep_read_status(ws) == ep.EP_OK and (ws[small:] == 255).all()
+    assert torch.equal(*outs)
