@@ -349,15 +349,22 @@ def _stream(stream):
 
 
 def _on_current_device(stream, *tensors) -> None:
-    """The calls run on the current device, unless the caller names a stream: refuses tensors of another one."""
+    """The calls run on the current device, unless the caller names a stream: refuses tensors of another one.  (Those of
+    the host are _arg's to refuse.)"""
     if stream is not None:
         return
-    import torch
-    here = torch.cuda.current_device() if any(t is not None and not isinstance(t, int) for t in tensors) else -1
+    here = None
     for t in tensors:
-        if t is not None and not isinstance(t, int) and t.get_device() != here:
-            raise ValueError(f"a tensor on device {t.get_device()} with device {here} current; "
-                             "use torch.cuda.device(...) around the call")
+        if t is None or isinstance(t, int):
+            continue
+        device = t.get_device()
+        if device != here and device >= 0:
+            if here is None:
+                import torch
+                here = torch.cuda.current_device()
+            if device != here:
+                raise ValueError(f"a tensor on device {device} with device {here} current; "
+                                 "use torch.cuda.device(...) around the call")
 
 
 def error_string(code: int) -> str:
@@ -675,7 +682,7 @@ def ep_expert_product_fp4(problem, product, x, expert_count, expert_offset, w_fp
     """ep_expert_product of up to EP_MOE_TOKENS_MAX tokens with MXFP4 weights:
     e2m1 codes, two a byte, and one e8m0 scale for each 32 of a row."""
     E, C, N, M, rows = _product_sizes(problem, product, expert_count)
-    _on_current_device(stream, x, w_fp4, w_sf, out)
+    _on_current_device(stream, x, expert_count, expert_offset, w_fp4, w_sf, bias, residual, out)
     return _run("ep_expert_product_fp4", problem, (_product_ref(product, bind), _arg(x, "x", "bf16", rows * C),
         _arg(expert_count, "expert_count", "int32", E), _arg(expert_offset, "expert_offset", "int32", E),
         _arg(w_fp4, "w_fp4", "e2m1", E * M * C // 2), _arg(w_sf, "w_sf", "e8m0", E * M * (C // 32)),
@@ -686,7 +693,7 @@ def ep_expert_product_fp4(problem, product, x, expert_count, expert_offset, w_fp
 def ep_moe_tokens_fp4(problem, product, x, topk_idx, topk_weights, w1_fp4, w1_sf, b1, w2_fp4, w2_sf, b2, residual, out,
                       workspace, workspace_bytes=None, stream=None, bind=False):
     """ep_moe_tokens with MXFP4 weights."""
-    _on_current_device(stream, x, w1_fp4, w2_fp4, out, workspace)
+    _on_current_device(stream, x, topk_idx, topk_weights, w1_fp4, w1_sf, b1, w2_fp4, w2_sf, b2, residual, out, workspace)
     return _run("ep_moe_tokens_fp4", problem, _tokens_ptrs(problem, product, x, topk_idx, topk_weights, w1_fp4, w1_sf,
         b1, w2_fp4, w2_sf, b2, residual, out, workspace, workspace_bytes, "e2m1", stream, bind), bind)
 
@@ -713,7 +720,8 @@ def ep_route(problem, router, logits, bias, token_mask, topk_idx, topk_weights, 
     """The router: top-k experts and their weights from the logits, and with
     the last arguments the counts, the balance loss and the z loss."""
     T, _, K, E, _, _, _ = _sizes(problem)
-    _on_current_device(stream, logits, topk_idx, topk_weights, workspace)
+    _on_current_device(stream, logits, bias, token_mask, topk_idx, topk_weights, expert_count, token_count, prob_sum, losses,
+                       workspace)
     return _run("ep_route", problem, (_product_ref(router, bind), _arg(logits, "logits", _logits_type(router), T * E),
         _arg(bias, "bias", "float", E), _arg(token_mask, "token_mask", "uint8", T),
         _arg(topk_idx, "topk_idx", "int32", T * K), _arg(topk_weights, "topk_weights", "float", T * K),
@@ -725,7 +733,7 @@ def ep_balance_loss(problem, router, logits, topk_idx, token_mask, expert_count,
                     workspace, workspace_bytes=None, stream=None, bind=False):
     """The counts, the balance loss and the z loss of choices made elsewhere."""
     T, _, K, E, _, _, _ = _sizes(problem)
-    _on_current_device(stream, logits, topk_idx, workspace)
+    _on_current_device(stream, logits, topk_idx, token_mask, expert_count, token_count, prob_sum, losses, workspace)
     return _run("ep_balance_loss", problem, (_product_ref(router, bind),
         _arg(logits, "logits", _logits_type(router), T * E), _arg(topk_idx, "topk_idx", "int32", T * K),
         _arg(token_mask, "token_mask", "uint8", T),
@@ -738,7 +746,7 @@ def ep_route_backward(problem, router, logits, topk_idx, token_mask, expert_coun
     """The logits' gradient from those of the weights (None: without) and of
     the two losses (None: without)."""
     T, _, K, E, _, _, _ = _sizes(problem)
-    _on_current_device(stream, logits, dweights, dlogits)
+    _on_current_device(stream, logits, topk_idx, token_mask, expert_count, token_count, dweights, dlosses, dlogits)
     return _run("ep_route_backward", problem, (_product_ref(router, bind),
         _arg(logits, "logits", _logits_type(router), T * E), _arg(topk_idx, "topk_idx", "int32", T * K),
         _arg(token_mask, "token_mask", "uint8", T), _arg(expert_count, "expert_count", "int32", E),
