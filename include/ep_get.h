@@ -182,9 +182,13 @@ size_t ep_route_workspace_bytes(const ep_problem *problem, const ep_router *rout
  * The order is that of the exact scores: without a bias of the logits
  * themselves, with one of sums in 64 bits.  An expert whose logit is -inf or
  * NaN, or whose sum is -inf or NaN, is never chosen; an entry that no expert
- * is left for is -1 with weight 0.  Sums are fp32 or wider; a NaN or +inf
- * logit makes the softmax of its token NaN, and with it the weights (but not
- * the normalised ones of other experts), prob_sum and losses.
+ * is left for is -1 with weight 0.  Sums are fp32 or wider.
+ * A NaN or +inf logit makes the softmax of its token NaN.  With softmax scores
+ * and a bias no expert of the token is then chosen; without a bias the
+ * weights are NaN, but that normalised ones are divided by the sum over the
+ * choices, and a NaN logit, never chosen, leaves them as they are.  Sigmoid
+ * scores are each of their own logit, 1 for +inf.  The z loss becomes NaN, and
+ * prob_sum and the balance loss too, but for +inf with sigmoid scores.
  * Only T, E and K of the problem are used; the other fields but S are checked.
  *
  *   logits       [T,E] fp32 or bf16 device (router->logits_bf16), 16-byte aligned
@@ -194,7 +198,7 @@ size_t ep_route_workspace_bytes(const ep_problem *problem, const ep_router *rout
  *   topk_idx     [T,K] int32 device, written
  *   topk_weights [T,K] fp32 device, written
  * and, for training, the statistics of the V tokens that count (those that
- * are no padding and have a logit above -inf), all four or all NULL:
+ * are no padding and have a logit above -inf or NaN), all four or all NULL:
  *   expert_count [E] int32  choices that name expert e
  *   token_count  [1] int32  V
  *   prob_sum     [E] fp32   sum over those tokens of p[t,e], p the softmax of
@@ -238,7 +242,8 @@ int ep_balance_loss(const ep_problem *problem, const ep_router *router, const vo
  *   dweights     [T,K] fp32 device (what ep_combine_backward gives), or NULL
  *   dlosses      [2] fp32 device, or NULL
  *   dlogits      [T,E] of the logits' type, 16-byte aligned, overwritten (0 for
- *                tokens that do not count); may be logits */
+ *                tokens that do not count, NaN for those with a NaN or +inf
+ *                logit); may be logits */
 int ep_route_backward(const ep_problem *problem, const ep_router *router, const void *logits,
                       const int32_t *topk_idx, const uint8_t *token_mask,
                       const int32_t *expert_count, const int32_t *token_count,
