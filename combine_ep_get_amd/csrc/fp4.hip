@@ -6,8 +6,9 @@
 //            out[t,:] = bf16(residual[t,:] + sum_j (W2[e] h[t,j,:] + w[t,j] b2[e]))
 //
 // Bound by the weights, each read once: 0.53 bytes a value.  A code and its scale
-// are widened to bf16 by one instruction for two, exactly, and multiplied by the
-// bf16 matrix instruction (its 16 rows are weight rows, its 16 columns tokens).
+// are widened to bf16 by one instruction for two, exactly (infinite from 2^128
+// on), and multiplied by the bf16 matrix instruction (its 16 rows are weight
+// rows, its 16 columns tokens).
 //
 // The matrix instruction's lane l has row l % 16 of a fragment, and the address
 // unit joins the accesses of neighbouring lanes only.  Loads in that order take

@@ -657,7 +657,9 @@ int ep_moe_tokens_fp8(const ep_problem *problem, const ep_product *product, cons
  * (0, 0.5, 1, 1.5, 2, 3, 4, 6 and, from code 8 on, their negatives) with one
  * scale byte (e8m0: 2^(byte - 127), 255 is NaN) for each 32 neighbours of a
  * row.  C and N are multiples of 32.  x stays bf16; a code with its scale is
- * widened to bf16, which holds it exactly (values below 2^-126 may count as 0).
+ * widened to bf16, which holds it exactly but at the ends of its range:
+ * values below 2^-126 may count as 0, and those of 2^128 and above (codes 4 and
+ * 6 at scale byte 253, 2 and above at 254) are infinite.
  *
  *   w_fp4 [E,M,C/2] uint8 device, 16-byte aligned; the value of an even c is
  *         in the low half of its byte
