@@ -692,17 +692,19 @@ size_t ep_grad_workspace_bytes(const ep_grad *grads, int32_t num_grads);
  *   norm       = sqrt(square_sum)
  *   out        = grad * min(1, max_norm / norm), rounded to its type
  * Squares and sums are 64-bit, in an order that does not change from call to
- * call.  Where the norm is not finite nothing is scaled: out = grad, and norm
- * tells.  A gradient that is its own out and needs no scaling is not touched.
- * The host array is read during the call and not kept.  Gradients may lie at
- * any address that their elements allow; no out overlaps another gradient or
- * out, or its own gradient unless it is the same.
+ * call.  Where square_sum is not finite, that is, some value is not, nothing
+ * is scaled: out = grad, and norm tells.  A gradient that is its own out and
+ * needs no scaling is not touched.  The host array is read during the call and
+ * not kept.  Gradients may lie at any address that their elements allow; no
+ * out overlaps another gradient or out, or its own gradient unless it is the
+ * same.
  *
  *   square_sum [1] fp64 device, overwritten by the first call
  *   workspace  ep_grad_workspace_bytes bytes, 256-byte aligned; calls that
  *              may overlap need one each
  *   max_norm   >= 0; infinity for no clipping
- *   norm       [1] fp32 device, written, or NULL */
+ *   norm       [1] fp32 device, written, or NULL; infinite also for a norm past
+ *              fp32's range, which scales as any other */
 int ep_grad_square_sum(const ep_grad *grads, int32_t num_grads, double *square_sum,
                        void *workspace, size_t workspace_bytes, void *stream);
 int ep_grad_clip(const ep_grad *grads, int32_t num_grads, const double *square_sum,

@@ -34,3 +34,14 @@ def test_factors_below_the_normal_numbers(ep, size, max_norm, shift):  # noqa: F
     # in place: the same bits
     clip(ep, grads, grads, max_norm)
     assert all(torch.equal(a, b) for a, b in zip(grads, outs))
+
+
+def test_norms_past_fp32(ep):  # noqa: F811
+    """A norm of 2^128 and more is finite in 64 bits and scales; only its fp32 output is infinite."""
+    grads = [torch.full((5000,), 2.0 ** 127, device="cuda"), torch.full((33,), -2.0 ** 127, device="cuda", dtype=BF)]
+    outs = [torch.empty_like(t) for t in grads]
+    norm, square = clip(ep, grads, outs, 4.0)
+    assert math.isinf(norm) and square == 5033 * 2.0 ** 254
+    want = 4.0 / math.sqrt(5033)
+    assert ((outs[0].double() - want).abs() <= want * 2.0 ** -23).all()
+    assert ((outs[1].double() + want).abs() <= want * (2.0 ** -23 + 2.0 ** -8)).all()
