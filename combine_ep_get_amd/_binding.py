@@ -153,6 +153,10 @@ class Grads:
             raise ValueError(f"outs: {len(outs)} tensors for {len(grads)} gradients")
         if len({t.device for t in (*grads, *outs)}) > 1:
             raise ValueError("gradients on more than one device: a list, and a sum, for each")
+        first = {}  # a gradient that is clipped twice at once has no defined result
+        for i, o in enumerate(outs):
+            if o.numel() and first.setdefault(o.data_ptr(), i) != i:
+                raise ValueError(f"outs: tensors {first[o.data_ptr()]} and {i} are the same memory")
         types = {torch.bfloat16: (EP_GRAD_BF16, "bf16"), torch.float32: (EP_GRAD_FP32, "float")}
         array = (Grad * len(grads))()
         for i, (g, o) in enumerate(zip(grads, outs)):
