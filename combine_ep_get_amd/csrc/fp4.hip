@@ -64,7 +64,8 @@ struct Rows {
     uint32_t w_at[2], sf_at, x_at[XC / 8];
 };
 
-// The weights of stage b.  FULL: no k of it is past K, of which there are zeros.  ONCE: no other wave reads them soon.
+// The weights of stage b.  FULL: no k of it is past K, of which there are zeros.  ONCE: past the caches, for weights that no
+// other wave reads soon.
 template <bool FULL, bool ONCE, int FF, int XC>
 __device__ __forceinline__ void load_weights(u32x4 (&w)[FF][2], uint32_t (&sf)[FF], const Rows<FF, XC> &r, int b, int K,
                                              const Lanes &ll) {
@@ -90,9 +91,12 @@ __device__ __forceinline__ void load_weights(u32x4 (&w)[FF][2], uint32_t (&sf)[F
     }
 }
 
+// Tiles of eight columns are for experts of which most have one tile; of sixteen an expert may have many, and each reads its
+// weights again (dense, weights from memory: 128 x 7168 x 2 x 2048 26.3 us, past the caches 32.1, 64 rows 18.1 and 20.7; of
+// one tile, 16 rows, 13.1 and 12.9).
 template <bool FULL, int FF, int XC>
 __device__ __forceinline__ void load_stage(Stage<FF, XC> &s, const Rows<FF, XC> &r, int b, int K, const Lanes &ll) {
-    load_weights<FULL, true>(s.w, s.sf, r, b, K, ll);
+    load_weights<FULL, XC == 8>(s.w, s.sf, r, b, K, ll);
     const char *x = r.x + static_cast<int64_t>(b) * (kStageK * 2);
 #pragma unroll
     for (int u = 0; u < 4; ++u)
