@@ -893,8 +893,12 @@ bool many(int64_t entries, int64_t E, int64_t outputs, bool gated) {
 // the chip one by one than by outputs, of which there are too few for all CUs, or some more than one each.  Us of layers
 // without and with it, of 2048 x 768: 2 tokens of 8 experts 25.1 and 25.1, 4 36.6 and 33.2, 64 tokens over 128 experts 106 and
 // 80; of 4672 x 704 over 64 experts 101 and 85, over 256 450 and 360; of 4096 x 1408, with an output tile for each CU, over 64
-// experts 134 and 138, over 128 289 and 285; a token of 8 experts 18.2 and 20.2.  Few tiles of a long k are as many where outputs are few: a token
-// of 7 experts of 832 x 3136 30.0 and 26.6; but 8 of 2880 x 2880 45.8 and 48.9.
+// experts 134 and 138, over 128 289 and 285; a token of 8 experts 18.2 and 20.2.  Where outputs just fall short of that, 64
+// tiles of 3200 x 1408 103 and 102, of 3232 110 and 112 (32 tiles 82 and 86, 89 and 92; 120 tiles 133 and 128, 144 and 139).
+// Few tiles of a long k are as many where outputs are few.  A token of 8 experts, of 1024 channels, 64 stages 21.1 and 20.8, 80
+// 24.2 and 22.8, 104 28.9 and 25.1; of 2048, 64 stages 23.9 and 24.6, 80 28.9 and 29.5, 104 34.5 and 33.5; of 2080, 104 stages
+// 40.6 and 43.6.  Two or three tokens, 96 stages of 2048 channels 34.5 and 33.0, 37.1 and 35.7; of 2080 40.2 and 40.2, 42.7 and 41.4;
+// 8 of 2880 x 2880 45.8 and 48.9.
 bool rows_apart(int64_t entries, int64_t E, int64_t H, int64_t I) {
     const int64_t tiles = max(min(entries, E), entries / 16), stages = tiles * ((I + kStageK - 1) / kStageK);
     const bool even = H > 16 * 200 && H <= 16 * kFp4Workgroups;
