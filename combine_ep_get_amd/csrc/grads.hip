@@ -56,29 +56,16 @@ __device__ __forceinline__ float element(const char *p, int64_t i, bool fp32) {
     return fp32 ? reinterpret_cast<const float *>(p)[i] : bf16_lo(reinterpret_cast<const uint16_t *>(p)[i]);
 }
 
-// What a gradient's values are multiplied by.  fp32 holds the factor but for its last rounding down to 2^-126; a smaller one,
-// of a norm of 2^126 times max_norm and more, would lose its digits or be 0, and multiplies in 64 bits.
-struct Factor {
-    bool scale, wide;  // whether anything is multiplied, and in 64 bits
-    float f;
-    double d;
-    __device__ __forceinline__ Factor(double norm, float max_norm) {
-        scale = norm > max_norm && norm < INFINITY;
-        d = scale ? max_norm / norm : 1.0;
-        f = static_cast<float>(d);
-        wide = d > 0.0 && d < 0x1p-126;
-    }
-    __device__ __forceinline__ float of(float v) const { return wide ? static_cast<float>(v * d) : v * f; }
-};
-
-// out[i] = p[i] times the factor, or its very bits
-__device__ __forceinline__ void move(char *out, const char *p, int64_t i, bool fp32, const Factor &by) {
+// out[i] = p[i] * f, or its very bits without `scale`.  V: float, or double for a factor that fp32 does not hold.
+template <class V>
+__device__ __forceinline__ void move(char *out, const char *p, int64_t i, bool fp32, bool scale, V f) {
     if (fp32) {
         const uint32_t v = reinterpret_cast<const uint32_t *>(p)[i];
-        reinterpret_cast<uint32_t *>(out)[i] = by.scale ? __float_as_uint(by.of(__uint_as_float(v))) : v;
+        reinterpret_cast<uint32_t *>(out)[i] = scale ? __float_as_uint(static_cast<float>(__uint_as_float(v) * f)) : v;
     } else {
         const uint16_t v = reinterpret_cast<const uint16_t *>(p)[i];
-        reinterpret_cast<uint16_t *>(out)[i] = by.scale ? __builtin_bit_cast(uint16_t, static_cast<__bf16>(by.of(bf16_lo(v)))) : v;
+        reinterpret_cast<uint16_t *>(out)[i] =
+            scale ? __builtin_bit_cast(uint16_t, static_cast<__bf16>(static_cast<float>(bf16_lo(v) * f))) : v;
     }
 }
 
@@ -173,19 +160,32 @@ __global__ __launch_bounds__(kGradThreads) void clip_kernel(GradTable t, const d
                                                             float *norm_out) {
     const double norm = sqrt(*square_sum);
     if (norm_out && blockIdx.x == 0 && threadIdx.x == 0) *norm_out = static_cast<float>(norm);
-    const Factor by(norm, max_norm);
+    const bool scale = norm > max_norm && norm < INFINITY;
+    const double factor = scale ? max_norm / norm : 1.0;
+    const float f = static_cast<float>(factor);
     const int pieces = t.first[t.num];
+    if (factor > 0.0 && factor < 0x1p-126) {
+        // fp32 holds a factor but for its last rounding down to 2^-126; a smaller one, of a norm of 2^126 times max_norm and
+        // more, would lose its digits there or be 0, and multiplies in 64 bits
+        for (int piece = blockIdx.x; piece < pieces; piece += gridDim.x) {
+            const int g = owner(t, piece);
+            const bool fp32 = t.fp32 >> g & 1;
+            const Span s = span_of(t.grad[g], t.count[g], piece - t.first[g], fp32 ? 4 : 2);
+            for (int64_t i = s.begin + threadIdx.x; i < s.end; i += kGradThreads) move(t.out[g], t.grad[g], i, fp32, true, factor);
+        }
+        return;
+    }
     for (int piece = blockIdx.x; piece < pieces; piece += gridDim.x) {
         const int g = owner(t, piece);
         const bool fp32 = t.fp32 >> g & 1;
         const char *p = t.grad[g];
         char *out = t.out[g];
-        if (!by.scale && out == p) continue;
+        if (!scale && out == p) continue;
         const int size = fp32 ? 4 : 2;
         Span s = span_of(p, t.count[g], piece - t.first[g], size);
-        if (by.wide || ((reinterpret_cast<uintptr_t>(p) ^ reinterpret_cast<uintptr_t>(out)) & 15)) {
-            // a product in 64 bits, or no 16-byte vector that is aligned on both sides
-            for (int64_t i = s.begin + threadIdx.x; i < s.end; i += kGradThreads) move(out, p, i, fp32, by);
+        if ((reinterpret_cast<uintptr_t>(p) ^ reinterpret_cast<uintptr_t>(out)) & 15) {
+            // no 16-byte vector is aligned on both sides
+            for (int64_t i = s.begin + threadIdx.x; i < s.end; i += kGradThreads) move(out, p, i, fp32, scale, f);
             continue;
         }
         const u32x4 *v = reinterpret_cast<const u32x4 *>(p + s.vec * size);
@@ -200,11 +200,11 @@ __global__ __launch_bounds__(kGradThreads) void clip_kernel(GradTable t, const d
 #pragma unroll
         for (int i = 0; i < kVectors; ++i) {
             const int at = threadIdx.x + i * kGradThreads;
-            if (at < n) __builtin_nontemporal_store(by.scale ? scaled(d[i], fp32, by.f) : d[i], o + at);
+            if (at < n) __builtin_nontemporal_store(scale ? scaled(d[i], fp32, f) : d[i], o + at);
         }
         const int64_t head = s.begin + threadIdx.x, tail = s.vec_end + threadIdx.x;
-        if (head < s.vec) move(out, p, head, fp32, by);
-        if (tail < s.end) move(out, p, tail, fp32, by);
+        if (head < s.vec) move(out, p, head, fp32, scale, f);
+        if (tail < s.end) move(out, p, tail, fp32, scale, f);
     }
 }
 
