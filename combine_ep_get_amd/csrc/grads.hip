@@ -12,7 +12,8 @@
 //
 // Both calls are bound by memory.  2.8 GB of gradients: the sum 480 us (5.9 TB/s), the clipping 1030 us, a read and a write
 // at 5.5 TB/s; together 1515 us with 4096 workgroups, 1538 with 2048.  The clipping's loads and stores are past the caches:
-// 1610 us with ordinary ones.  40 small gradients: 5, 2 and 7 us, launches for the most part.
+// 1610 us with ordinary ones.  40 small gradients: 5, 3 and 7 us, of which a launch is 2; the rest is 144 workgroups with
+// one piece each, which wait for the search of its gradient in the arguments, then for its loads, with nothing behind them.
 #include <algorithm>
 
 #include "../../include/ep_get.h"

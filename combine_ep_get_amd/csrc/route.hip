@@ -9,10 +9,12 @@
 // reduction over a token is four DPP moves); everything else follows from
 // these registers, so the logits are read once.
 //
-// Small calls are one short kernel, or two where statistics are joined: 5 us each, of which 2 are a launch.  Large ones
-// are bound by instructions.  16384 tokens of 256 fp32 experts: the choice of 8 with a bias and statistics 16 us, and 5 to
-// join them, where the logits' 17 MB take 3.6 at the rate of a copy; the gradient 10 to 11 us (7.2).  16384 tokens of 64
-// experts: statistics of given choices 5 and 5 us.
+// Small calls are one short kernel, or two where statistics are joined: 5 us each, of which 2 are a launch.  16384 tokens of
+// 256 fp32 experts, whose logits' 17 MB take 3.6 us at the rate of a copy: the choice of 8 takes 9.8 us, by sigmoid and a
+// bias 11.9, with statistics 16, and 5 to join them.  Those 16 us are 9 of instructions, and waits (56 % of the waves' cycles)
+// for the rounds of the choice, each of which needs the one before, and for loads: a wave has its four tokens once, with
+// one workgroup a CU, so nothing else covers them.  The gradient takes 10 to 11 us (7.2).  16384 tokens of 64 experts:
+// statistics of given choices 5 and 5 us.
 #include <limits.h>
 
 #include <algorithm>
@@ -578,7 +580,9 @@ __global__ __launch_bounds__((kThreads<MODE, L, N>)) void route_kernel(RouteArgs
 }
 
 // Joins the partial sums: 16 experts a workgroup, its rows the partials in
-// turn; the last workgroup to finish adds up the losses.  5 us for 256 partials
+// turn; the last workgroup to finish adds up the losses.  The workgroups' sums of
+// probabilities are fp32, and so is what prob_sum holds and the balance loss is
+// made of: a rounding each, of the size of prob_sum's own.  5 us for 256 partials
 // of 256 experts: a launch, a read and the ticket, one after the other.
 constexpr int kJoinThreads = 1024;
 constexpr int kJoinColumns = 16;
